@@ -62,6 +62,16 @@ SIGNATURES = {
     "dsa_indexer_topk_reuse": (ctypes.c_int, [_vp, _i64, _vp, _i64, _vp, _vp, _vp, _vp, _vp]),
     "dsa_indexer_sparse_mla": (ctypes.c_int, [_vp, _i64, _vp, _i32, _vp, _i64, _vp, _vp, _i32, _vp, _i32,
                                               ctypes.c_float, _vp, _vp, _vp]),
+    "dsa_indexer_latent_attention_workspace": (_i64, [_vp, _i64, _i32, _i32]),
+    "dsa_indexer_latent_attention": (ctypes.c_int, [_vp, _i64, _vp, _i32, _vp, _i64, _vp, _vp, _i32, _vp, ctypes.c_float,
+                                                    _vp, _vp, _vp, _i64, _vp]),
+    "dsa_indexer_latent_attention_fp4": (ctypes.c_int, [_vp, _i64, _vp, _i32, _vp, _i64, _vp, _vp, _i32, _vp, _vp, _i32,
+                                                        ctypes.c_float, _vp, _vp, _vp, _i64, _vp]),
+    "dsa_indexer_quantize_latent_fp4": (ctypes.c_int, [_vp, _i64, _vp, _vp, _vp, _i64, _vp]),
+    "dsa_indexer_dequantize_latent_fp4": (ctypes.c_int, [_vp, _i64, _vp, _i64, _vp, _vp, _vp]),
+    "dsa_indexer_latent_expanded_workspace": (_i64, [_vp, _i64, _i32, _i32, _i64]),
+    "dsa_indexer_latent_attention_expanded": (ctypes.c_int, [_vp, _i64, _vp, _i32, _vp, _i64, _vp, _vp, _vp, _i32, _vp,
+                                                             ctypes.c_float, _vp, _vp, _i64, _vp]),
     "dsa_indexer_device_error": (ctypes.c_int, [_vp]),
     "dsa_indexer_noalloc_device_error": (ctypes.c_int, [_vp]),
     "dsa_indexer_selftest_wait_timeout": (ctypes.c_int, [_i64, _vp]),

@@ -275,6 +275,139 @@ class Indexer:
               "dsa_indexer_sparse_mla")
         return out, lse
 
+    # ------------------------------------------------------------------ latent cache: dense, 4-bit, prompts
+    def _latent_common(self, q, dim, positions, q_seq_offsets, cache_offsets, kv, kv_dtype, kv_dim):
+        dev = self.device
+        _need(q, "q", torch.bfloat16, dev)
+        _need(kv, "kv_cache", kv_dtype, dev)
+        if q.dim() != 3 or q.shape[1] < 1 or q.shape[2] != dim or kv.dim() != 2 or kv.shape[1] != kv_dim:
+            raise ValueError(f"q must be [T, H, {dim}] and kv_cache [rows, {kv_dim}]")
+        _need(q_seq_offsets, "q_seq_offsets", torch.int32, dev)
+        _need(cache_offsets, "cache_offsets", torch.int64, dev)
+        if q_seq_offsets.dim() != 1 or q_seq_offsets.numel() < 2 or cache_offsets.shape != q_seq_offsets.shape:
+            raise ValueError("q_seq_offsets and cache_offsets must be [B + 1] with B >= 1")
+        if positions is not None:
+            _need(positions, "positions", torch.int32, dev)
+            if positions.shape != q.shape[:1]:
+                raise ValueError("positions must be [T]")
+        return q.shape[0], q.shape[1], q_seq_offsets.numel() - 1
+
+    def _out(self, t, name, dtype, shape):
+        if t is None:
+            return torch.empty(shape, dtype=dtype, device=self.device)
+        _need(t, name, dtype, self.device)
+        if tuple(t.shape) != tuple(shape):
+            raise ValueError(f"{name} must be {list(shape)}")
+        return t
+
+    def _on(self, stream):
+        """The stream of a call, current for its allocations (torch's allocator then reuses its
+        workspace only behind the call)."""
+        return torch.cuda.stream(torch.cuda.current_stream(self.device) if stream is None else stream)
+
+    def _latent(self, q, kv, fp4, positions, q_seq_offsets, cache_offsets, scale, idx, out, lse, stream):
+        T, H, B = self._latent_common(q, 576, positions, q_seq_offsets, cache_offsets, kv,
+                                      torch.uint8 if fp4 else torch.bfloat16, 416 if fp4 else 576)
+        k_sel = -1
+        if idx is not None:
+            _need(idx, "idx", torch.int32, self.device)
+            if idx.dim() != 2 or idx.shape[0] != T:
+                raise ValueError("idx must be [T, k_sel]")
+            k_sel = idx.shape[1]
+        elif positions is None:
+            raise ValueError("positions are needed without idx")
+        with torch.cuda.device(self.device), self._on(stream):
+            out = self._out(out, "out", torch.bfloat16, (T, H, 512))
+            lse = self._out(lse, "lse", torch.float32, (T, H))
+            n = self._lib.dsa_indexer_latent_attention_workspace(self._h, T, B, H)
+            ws = torch.empty(max(n, 16), dtype=torch.uint8, device=self.device)
+            rest = (float(scale), _ptr(out), _ptr(lse), _ptr(ws), ws.numel(), _stream(None))
+            head = (self._h, T, _ptr(q), H, _ptr(kv), kv.shape[0], _ptr(positions), _ptr(q_seq_offsets), B,
+                    _ptr(cache_offsets))
+            if fp4:
+                check(self._lib.dsa_indexer_latent_attention_fp4(*head, _ptr(idx), k_sel, *rest),
+                      "dsa_indexer_latent_attention_fp4")
+            else:
+                check(self._lib.dsa_indexer_latent_attention(*head, *rest), "dsa_indexer_latent_attention")
+        return out, lse
+
+    def latent_attention(self, q, kv_cache, positions, q_seq_offsets, cache_offsets, scale, out=None, lse=None,
+                         stream=None):
+        """Dense attention in the absorbed form: query t (q bf16 [T, H, 576]) attends to rows
+        0..positions[t] of its sequence in kv_cache (bf16 [rows, 576]); returns out bf16
+        [T, H, 512] and lse fp32 [T, H].  Serves prompt chunks, drafted tokens and single tokens."""
+        return self._latent(q, kv_cache, False, positions, q_seq_offsets, cache_offsets, scale, None, out, lse, stream)
+
+    def latent_attention_fp4(self, q, kv_cache_fp4, positions, q_seq_offsets, cache_offsets, scale, idx=None, out=None,
+                             lse=None, stream=None):
+        """latent_attention over a 4-bit cache (uint8 [rows, 416], see quantize_latent_fp4): the
+        whole prefix, or with idx (int32 [T, k_sel], -1 = none, as topk returns it) the selected
+        positions; positions may then be None."""
+        return self._latent(q, kv_cache_fp4, True, positions, q_seq_offsets, cache_offsets, scale, idx, out, lse,
+                            stream)
+
+    def quantize_latent_fp4(self, kv, out=None, rows=None, stream=None):
+        """4-bit rows (uint8 [n, 416]) of bf16 latent rows kv [n, 576]; with out (a cache) and
+        rows (int64 [n], distinct), row i goes to out[rows[i]].  Returns out."""
+        dev = self.device
+        _need(kv, "kv", torch.bfloat16, dev)
+        if kv.dim() != 2 or kv.shape[1] != 576:
+            raise ValueError("kv must be [n, 576]")
+        n = kv.shape[0]
+        if rows is not None:
+            _need(rows, "rows", torch.int64, dev)
+            if rows.shape != (n,) or out is None:
+                raise ValueError("rows must be [n] and come with out")
+        with torch.cuda.device(dev), self._on(stream):
+            if out is None:
+                out = torch.empty((n, 416), dtype=torch.uint8, device=dev)
+            _need(out, "out", torch.uint8, dev)
+            if out.dim() != 2 or out.shape[1] != 416 or (rows is None and out.shape[0] < n):
+                raise ValueError("out must be [rows, 416] with room for every row of kv")
+            check(self._lib.dsa_indexer_quantize_latent_fp4(self._h, n, _ptr(kv), _ptr(rows), _ptr(out), out.shape[0],
+                                                            _stream(None)), "dsa_indexer_quantize_latent_fp4")
+        return out
+
+    def dequantize_latent_fp4(self, kv_fp4, rows=None, out=None, stream=None):
+        """The bf16 values [n, 576] that the rows of a 4-bit cache (or its rows `rows`, int64 [n])
+        stand for."""
+        dev = self.device
+        _need(kv_fp4, "kv_fp4", torch.uint8, dev)
+        if kv_fp4.dim() != 2 or kv_fp4.shape[1] != 416:
+            raise ValueError("kv_fp4 must be [rows, 416]")
+        if rows is not None:
+            _need(rows, "rows", torch.int64, dev)
+            if rows.dim() != 1:
+                raise ValueError("rows must be [n]")
+        n = kv_fp4.shape[0] if rows is None else rows.numel()
+        with torch.cuda.device(dev), self._on(stream):
+            out = self._out(out, "out", torch.bfloat16, (n, 576))
+            check(self._lib.dsa_indexer_dequantize_latent_fp4(self._h, n, _ptr(kv_fp4), kv_fp4.shape[0], _ptr(rows),
+                                                              _ptr(out), _stream(None)),
+                  "dsa_indexer_dequantize_latent_fp4")
+        return out
+
+    def latent_attention_expanded(self, q, kv_cache, W_ukv, positions, q_seq_offsets, cache_offsets, scale, out=None,
+                                  stream=None):
+        """Attention in the expanded form, for prompts: q bf16 [T, H, 192], the cache rows of the
+        call's sequences kv_cache bf16 [rows, 576], W_ukv bf16 [H, 256, 512] (each head's 128 key
+        rows, then its 128 value rows); returns out bf16 [T, H, 128]."""
+        T, H, B = self._latent_common(q, 192, positions, q_seq_offsets, cache_offsets, kv_cache, torch.bfloat16, 576)
+        _need(W_ukv, "W_ukv", torch.bfloat16, self.device)
+        if W_ukv.shape != (H, 256, 512):
+            raise ValueError("W_ukv must be [H, 256, 512]")
+        if positions is None:
+            raise ValueError("positions are needed")
+        with torch.cuda.device(self.device), self._on(stream):
+            out = self._out(out, "out", torch.bfloat16, (T, H, 128))
+            n = self._lib.dsa_indexer_latent_expanded_workspace(self._h, T, B, H, kv_cache.shape[0])
+            ws = torch.empty(max(n, 16), dtype=torch.uint8, device=self.device)
+            check(self._lib.dsa_indexer_latent_attention_expanded(
+                self._h, T, _ptr(q), H, _ptr(kv_cache), kv_cache.shape[0], _ptr(W_ukv), _ptr(positions),
+                _ptr(q_seq_offsets), B, _ptr(cache_offsets), float(scale), _ptr(out), _ptr(ws), ws.numel(),
+                _stream(None)), "dsa_indexer_latent_attention_expanded")
+        return out
+
     def device_error(self) -> int:
         """Synchronises and returns (then clears) the handle's device error status."""
         with torch.cuda.device(self.device):

@@ -289,6 +289,89 @@ dsa_status_t dsa_indexer_sparse_mla(dsa_indexer_t h, int64_t T, const void* q, i
                                     int32_t B, const int32_t* idx, int32_t k_sel, float scale, void* out, float* lse,
                                     void* stream);
 
+/* ---- Dense attention over the latent cache ('Latent attention (MLA)' row, as for
+ * dsa_indexer_sparse_mla, of which these are the forms without the indexer's selection,
+ * over a cache held in 4 bits, and for prompts).  Common rules:
+ *   positions     int32 [T]; query t at position p attends to its sequence's rows 0..p.
+ *                 p = -1: the query attends to nothing (out = 0, lse = -inf, no error)
+ *   q_seq_offsets, cache_offsets: as for dsa_indexer_project.  Tokens below q_seq_offsets[0]
+ *                 or at or past q_seq_offsets[B] belong to no sequence (a batch padded to a
+ *                 fixed T): their rows of out and lse are left as they were
+ *   n_heads       1..1024, and T * n_heads <= 2^30;  scale > 0
+ *   workspace     device memory of at least the stated size, 16-byte aligned, its contents
+ *                 free; the call reads none of what an earlier call left there.  Calls that
+ *                 may overlap on the GPU need a workspace each
+ * A position outside [-1, rows of the sequence) gives out = 0 and lse = -inf and sets
+ * DSA_ERR_DEVICE_BOUNDS; malformed offsets set it too and give every query of the call out = 0
+ * and lse = -inf.  Cache rows past a sequence's largest queried position are never used,
+ * whatever they hold; a row that one of a sequence's queries attends to must hold finite
+ * values for the sequence's other queries to be defined.  Scores, softmax statistics and
+ * outputs are accumulated in fp32; the weights multiply the values as bf16, and out is rounded
+ * to bf16 once.  T = 0 is a no-op; asynchronous on `stream`. */
+
+/* Bytes of workspace that dsa_indexer_latent_attention and _latent_attention_fp4 need for T
+ * tokens of n_heads heads in B sequences (-1 for a bad argument). */
+int64_t dsa_indexer_latent_attention_workspace(dsa_indexer_t h, int64_t T, int32_t B, int32_t n_heads);
+
+/* Absorbed form over a bf16 cache: prompt chunks, drafted tokens and single decode tokens.
+ *   q bf16 [T, n_heads, 576], kv_cache bf16 [cache_rows, 576]
+ *   x[t,h,s] = scale * (q[t,h] . kv[s]),  out[t,h] = sum_s softmax_s(x) kv[s][0..511]
+ *   out bf16 [T, n_heads, 512], lse fp32 [T, n_heads] = ln sum_s exp(x[t,h,s]) */
+dsa_status_t dsa_indexer_latent_attention(dsa_indexer_t h, int64_t T, const void* q, int32_t n_heads,
+                                          const void* kv_cache, int64_t cache_rows, const int32_t* positions,
+                                          const int32_t* q_seq_offsets, int32_t B, const int64_t* cache_offsets,
+                                          float scale, void* out, float* lse, void* workspace,
+                                          int64_t workspace_bytes, void* stream);
+
+/* A cache held in 4 bits: uint8 [cache_rows, 416].  A row is 256 bytes of e2m1 codes of the
+ * 512-value latent (two a byte, the first in the low nibble), 32 e4m3 scales, one for each
+ * block of 16 values, and the 64-value rope key in bf16 (128 bytes).  A block's scale is
+ * s = e4m3(min(amax / 6, 448)) and its codes e2m1(x / s), to nearest, ties to the even code,
+ * saturating at 6 s; s = 0 stores zeros.  The value stood for is code * s, exact in bf16.
+ * kv bf16 [n, 576] holds finite values. */
+
+/* Row i of kv goes to row rows[i] of out (rows int64 [n], distinct), or to row i when rows is
+ * NULL.  A row outside [0, out_rows) is not written and sets DSA_ERR_DEVICE_BOUNDS. */
+dsa_status_t dsa_indexer_quantize_latent_fp4(dsa_indexer_t h, int64_t n, const void* kv, const int64_t* rows,
+                                             void* out, int64_t out_rows, void* stream);
+
+/* The values that rows rows[i] (or 0..n-1 when rows is NULL) of a 4-bit cache of kv_rows rows
+ * stand for: out bf16 [n, 576].  A row outside [0, kv_rows) reads as zeros and sets
+ * DSA_ERR_DEVICE_BOUNDS. */
+dsa_status_t dsa_indexer_dequantize_latent_fp4(dsa_indexer_t h, int64_t n, const void* kv_fp4, int64_t kv_rows,
+                                               const int64_t* rows, void* out, void* stream);
+
+/* dsa_indexer_latent_attention over a 4-bit cache.  k_sel < 0: dense (idx is not read).
+ * k_sel >= 0: over the indexer's selection, idx int32 [T, k_sel], positions in the query's
+ * sequence, -1 = no token, a repeated position counting once per entry (positions may be NULL);
+ * an entry at or past its sequence's row count is skipped and sets DSA_ERR_DEVICE_BOUNDS. */
+dsa_status_t dsa_indexer_latent_attention_fp4(dsa_indexer_t h, int64_t T, const void* q, int32_t n_heads,
+                                              const void* kv_cache_fp4, int64_t cache_rows, const int32_t* positions,
+                                              const int32_t* q_seq_offsets, int32_t B, const int64_t* cache_offsets,
+                                              const int32_t* idx, int32_t k_sel, float scale, void* out, float* lse,
+                                              void* workspace, int64_t workspace_bytes, void* stream);
+
+/* Bytes of workspace of dsa_indexer_latent_attention_expanded (-1 for a bad argument): the keys
+ * and values of every cache row (cache_rows * n_heads * 512 bytes) and a plan. */
+int64_t dsa_indexer_latent_expanded_workspace(dsa_indexer_t h, int64_t T, int32_t B, int32_t n_heads,
+                                              int64_t cache_rows);
+
+/* Expanded form, for prompts: each head's keys and values are up-projected from the latent.
+ *   q     bf16 [T, n_heads, 192] (128 values without a rotary step, then 64 rope values)
+ *   kv_cache bf16 [cache_rows, 576], W_ukv bf16 [n_heads, 256, 512] (a head's 128 key rows, then
+ *         its 128 value rows; out x in)
+ *   k[s,h] = bf16(W_ukv[h][0..127] kv[s][0..511]) | kv[s][512..575],
+ *   v[s,h] = bf16(W_ukv[h][128..255] kv[s][0..511]),
+ *   out[t,h] = sum_s softmax_s(scale * (q[t,h] . k[s,h])) v[s,h],  bf16 [T, n_heads, 128]
+ * Every one of the cache_rows rows is expanded: pass the part of the cache that holds the
+ * call's sequences, with cache_offsets counted from its first row (at most 8,388,480 rows;
+ * more: DSA_ERR_UNSUPPORTED). */
+dsa_status_t dsa_indexer_latent_attention_expanded(dsa_indexer_t h, int64_t T, const void* q, int32_t n_heads,
+                                                   const void* kv_cache, int64_t cache_rows, const void* W_ukv,
+                                                   const int32_t* positions, const int32_t* q_seq_offsets, int32_t B,
+                                                   const int64_t* cache_offsets, float scale, void* out,
+                                                   void* workspace, int64_t workspace_bytes, void* stream);
+
 /* Synchronises the device, then returns DSA_OK or the first device-side error
  * recorded since the last call (DSA_ERR_DEVICE_BOUNDS, DSA_ERR_DEVICE_TIMEOUT)
  * and clears the error word. */

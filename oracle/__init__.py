@@ -35,3 +35,10 @@ from .sparse_mla_oracle import (  # noqa: F401
     MLA_LATENT,
     sparse_mla,
 )
+from .latent_oracle import (  # noqa: F401
+    FP4_GRID,
+    FP4_ROW_BYTES,
+    latent_attention,
+    latent_attention_expanded,
+    quantize_latent_fp4,
+)
