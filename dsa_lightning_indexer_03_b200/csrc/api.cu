@@ -408,7 +408,11 @@ dsa_status_t latent_impl(dsa_indexer_t h, int64_t T, const void* q, int32_t n_he
   a.num_sms = h->num_sms;
   a.err = h->ws.err;
   a.timeout_ns = timeout_ns();
-  return launch_latent_attention(a, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+  CUtensorMap tmQ, tmC;
+  if (!make_tmap(&tmQ, q, kLatDim, uint64_t(T) * n_heads, 64, 96)) return DSA_ERR_INVALID_ARG;
+  if (fp4) tmC = tmQ;
+  else if (!make_tmap(&tmC, kv, kLatDim, uint64_t(cache_rows), 64, 64)) return DSA_ERR_INVALID_ARG;
+  return launch_latent_attention(a, tmQ, tmC, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
 }  // namespace

@@ -43,7 +43,10 @@ struct LatentArgs {
 };
 
 int64_t latent_workspace_bytes(int64_t T, int64_t B, int64_t H, int num_sms);
-cudaError_t launch_latent_attention(const LatentArgs& a, cudaStream_t s);
+// tmQ: bf16 [T * H, 576], boxes of 64 values x 96 rows; tmC: the bf16 cache [cache_rows, 576],
+// boxes of 64 values x 64 rows (not read when fp4)
+cudaError_t launch_latent_attention(const LatentArgs& a, const CUtensorMap& tmQ, const CUtensorMap& tmC,
+                                    cudaStream_t s);
 
 // 4-bit rows of n bf16 rows kv [n, 576]: row i goes to row rows[i] of out (row i without rows)
 cudaError_t launch_quantize_latent_fp4(int64_t n, const void* kv, const int64_t* rows, uint8_t* out, int64_t out_rows,

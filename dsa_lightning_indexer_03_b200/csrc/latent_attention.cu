@@ -1,142 +1,1142 @@
-// latent_attention.cu -- dense (and, over a 4-bit cache, selected) attention in the absorbed
-// form of multi-head latent attention.
+// latent_attention.cu -- dense attention in the absorbed form of multi-head latent attention,
+// over a bf16 or a 4-bit cache, and over the indexer's selection of a 4-bit cache.
 //
-//   x[t,h,s] = scale * (q[t,h] . c[s])  over the 576 cached values,
-//   out[t,h] = sum_s softmax_s(x) * c[s][0..511],   lse[t,h] = ln sum_s exp(x[t,h,s]).
+//   x[r,s] = scale * (q[r] . c[s])  over the 576 cached values of a token,
+//   out[r] = sum_s softmax_s(x[r]) c[s][0..511],   lse[r] = ln sum_s exp(x[r,s]),
 //
-// First form: one warp per (token, head), an online softmax over the tokens it attends to.
+// for the rows r = (token, head) of a sequence.  All rows of a sequence read the same cache
+// rows, so they are taken in groups of up to 96 consecutive rows (one decode token of 96 heads,
+// or several tokens of fewer), and a group's tokens in tiles of 128.
+//
+// The products run transposed: S^T = C . Q^T (M = 128 tokens, N = the group's rows, K = 576)
+// and O^T += C_latent^T . P^T (M = 4 x 128 latent dims, N = rows, K = 128 tokens).  So M is
+// always full (96 rows as M would waste a quarter of it), the whole 512-dim output of a group
+// (4 x 96 fp32 columns) and its scores (96) fit in one SM's TMEM, and the scores of a tile are
+// computed once.  Q (96 x 576, 108 KB) stays in shared memory; the cache streams through a ring
+// of 16 KB stages: nine 64-value chunks of a tile for its scores, then the tile again (from L2)
+// as eight 64-token x 128-dim pieces for its values, since Q and a whole 144 KB tile do not fit
+// together.
+//
+// latent_attention_kernel: persistent, one block of 16 warps per SM.
+//   warps 0-3   fill the ring: one thread with TMA (bf16), or all by converting 4-bit rows; for
+//               bf16 warp 2 zeroes the rows behind a sequence's last token (0 * NaN is NaN).
+//   warps 4-11  softmax: a thread per token, half of the rows each.  The reference m of a row
+//               is its running maximum, raised only when a score exceeds it by more than 8 (log2
+//               units, so weights stay below 256): most tiles then need no maximum over the
+//               tokens, which lie across threads, only a vote.  Sums are kept per thread and
+//               added up at the end.  Weights go to shared memory as bf16 (the MMA's operand).
+//   warp 12     (of a warpgroup that otherwise idles) issues the MMAs: S(t+1) before the values of t, so that the softmax of a tile
+//               runs under the MMAs of its neighbours.
+// Work: plan_kernel lists the groups and their tiles; the blocks take equal shares of all tiles
+// in order, so a share may begin or end inside a group; such pieces leave unnormalised fp32
+// sums and (m, l) in the workspace, which merge_kernel joins in a fixed order.
+//
+// A row of a bf16 cache that only some of a tile's queries may see can hold NaN or infinities; its
+// weight for the others is 0, and 0 * NaN spoils their sums.  Such rows of out (NaN under a
+// finite sum of weights) are listed and computed again by merge_kernel over their own prefix.
+//
+// Bound: 1,152 B (bf16) and 2 * 96 * 1,088 flop a cached token at 96 rows; on chip, 765 KB
+// of shared-memory traffic a tile (operands of both products and the ring's writes).
 
 #include "latent.h"
 
 namespace dsa {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kRows = 96;                    // rows (token, head) of a group
+constexpr int kTile = 128;                   // tokens of a tile
+constexpr int kQChunk = kRows * 128;         // 64 values of each row of Q
+constexpr int kQBytes = 9 * kQChunk;
+constexpr int kStages = 5;
+constexpr int kStage = 16384;
+constexpr int kPHalf = kTile * 128;          // weights of 64 rows: 128 tokens x 128 B
+constexpr int kFillWarps = 4, kSoftWarps = 8, kMmaWarp = 12, kThreads = 16 * 32;
+// registers a thread: 128 at launch, then 96 (fill), 184 (softmax), 48 (MMA): 4 * 96 + 8 * 184 + 4 * 48 = 16 * 128
+constexpr int kFillRegs = 96, kSoftRegs = 184, kMmaRegs = 48;
+constexpr uint32_t kTmemS = 4 * kRows;       // O^T block j at 96 j, the scores behind them
+constexpr uint64_t kDrainNs = 200ull * 1000 * 1000;
+constexpr float kUnset = -1e38f;             // reference of a row without a token so far
+constexpr int64_t kSlotFloats = kRows * kLatV;
 
-__device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
+struct Group {
+  int64_t kv_row0;     // cache row of the sequence's token 0
+  int32_t row0;        // first row (token * H + head)
+  int32_t nrows;
+  int32_t seq_len;     // cache rows of the sequence
+  int32_t ntok;        // tokens any of the rows attends to (dense), or entries of the idx row
+  int32_t pad0, pad1;
+};
 
-// Are the offsets well formed?  (q_seq_offsets within [0, T] and non-decreasing, cache_offsets
-// within [0, cache_rows] and non-decreasing)
-__global__ void check_offsets_kernel(LatentArgs a, int* bad) {
-  int b_bad = 0;
-  for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
-    const int64_t q0 = a.q_seq_offsets[b], q1 = a.q_seq_offsets[b + 1];
-    const int64_t c0 = a.cache_offsets[b], c1 = a.cache_offsets[b + 1];
-    if (q0 < 0 || q1 < q0 || q1 > a.T || c0 < 0 || c1 < c0 || c1 > a.cache_rows) b_bad = 1;
+struct Plan {          // header of the workspace
+  int64_t tiles;       // over all groups
+  int32_t groups;
+  int32_t bad;         // malformed offsets
+  int32_t spoiled;     // entries of Ws::spoiled
+};
+
+struct Ws {
+  Plan* plan;
+  int32_t* seq_group;   // [B+1] first group of each sequence
+  Group* group;         // [max groups]
+  int64_t* tile0;       // [max groups + 1] first tile of each group
+  int32_t* spoiled;     // [T * H] rows of out to compute again
+  float2* ml;           // [2 * blocks][96] reference and sum of the piece's rows
+  float* o;             // [2 * blocks][96][512]
+  int64_t max_groups;
+  int64_t bytes;
+};
+
+// Groups: rows / 96 and one more ragged one per sequence (dense), or per token (selection).
+int64_t max_groups(int64_t T, int64_t B, int64_t H) {
+  const int64_t dense = T * H / kRows + (B < T ? B : T) + 1, sel = T * ((H + kRows - 1) / kRows);
+  return dense > sel ? dense : sel;
+}
+
+Ws carve(void* base, int64_t T, int64_t B, int64_t H, int blocks) {
+  Ws w;
+  w.max_groups = max_groups(T, B, H);
+  int64_t off = 0;
+  auto take = [&](int64_t bytes) {
+    uint8_t* p = static_cast<uint8_t*>(base) + off;
+    off = (off + bytes + 255) & ~int64_t(255);
+    return p;
+  };
+  w.plan = reinterpret_cast<Plan*>(take(sizeof(Plan)));
+  w.seq_group = reinterpret_cast<int32_t*>(take(4 * (B + 1)));
+  w.group = reinterpret_cast<Group*>(take(sizeof(Group) * w.max_groups));
+  w.tile0 = reinterpret_cast<int64_t*>(take(8 * (w.max_groups + 1)));
+  w.spoiled = reinterpret_cast<int32_t*>(take(4 * T * H));
+  w.ml = reinterpret_cast<float2*>(take(sizeof(float2) * kRows * 2 * blocks));
+  w.o = reinterpret_cast<float*>(take(4 * kSlotFloats * 2 * blocks));
+  w.bytes = off;
+  return w;
+}
+
+struct Params {
+  int T, B, H, k_sel;
+  int64_t cache_rows;
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* kv;     // bf16 cache, or
+  const uint8_t* kv4;          // 4-bit cache
+  const int32_t* positions;
+  const int32_t* q_seq_offsets;
+  const int64_t* cache_offsets;
+  const int32_t* idx;
+  float scale_log2;
+  __nv_bfloat16* out;
+  float* lse;
+  Ws ws;
+  int* err;
+  uint64_t timeout_ns;
+};
+
+// ---------------------------------------------------------------- plan
+constexpr int kPlanThreads = 1024;
+
+// Inclusive prefix sum over the block's 1,024 threads (all of them call it).
+__device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_sums) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) {
+    const int64_t o = __shfl_up_sync(0xffffffffu, v, d);
+    if (lane >= d) v += o;
   }
-  b_bad = __syncthreads_or(b_bad);
-  if (threadIdx.x == 0) {
-    *bad = b_bad;
-    if (b_bad) atomicOr(a.err, kErrOffsets);
+  __syncthreads();
+  if (lane == 31) warp_sums[warp] = v;
+  __syncthreads();
+  if (warp == 0) {
+    int64_t s = warp_sums[lane];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t o = __shfl_up_sync(0xffffffffu, s, d);
+      if (lane >= d) s += o;
+    }
+    warp_sums[lane] = s;
+  }
+  __syncthreads();
+  return v + (warp ? warp_sums[warp - 1] : 0);
+}
+
+__global__ void __launch_bounds__(kPlanThreads) latent_plan_kernel(Params p) {
+  __shared__ int64_t sums[32];
+  const Ws& w = p.ws;
+  const int tid = threadIdx.x;
+  int bad = 0;
+  for (int b = tid; b < p.B; b += kPlanThreads) {
+    const int64_t q0 = p.q_seq_offsets[b], q1 = p.q_seq_offsets[b + 1];
+    const int64_t c0 = p.cache_offsets[b], c1 = p.cache_offsets[b + 1];
+    if (q0 < 0 || q1 < q0 || q1 > p.T || c0 < 0 || c1 < c0 || c1 > p.cache_rows) bad = 1;
+  }
+  bad = __syncthreads_or(bad);
+  if (bad) {   // merge_kernel writes every row as attending to nothing
+    if (tid == 0) {
+      w.plan->tiles = 0;
+      w.plan->groups = 0;
+      w.plan->bad = 1;
+      w.plan->spoiled = 0;
+      atomicOr(p.err, kErrOffsets);
+    }
+    return;
+  }
+  const int per_tok = (p.H + kRows - 1) / kRows;   // groups of a token (selection)
+  int64_t base = 0;
+  for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
+    const int b = b0 + tid;
+    int64_t n = 0;
+    if (b < p.B) {
+      const int64_t nq = p.q_seq_offsets[b + 1] - p.q_seq_offsets[b];
+      n = p.k_sel >= 0 ? nq * per_tok : (nq * p.H + kRows - 1) / kRows;
+    }
+    const int64_t inc = block_scan(n, sums);
+    if (b < p.B) w.seq_group[b + 1] = static_cast<int32_t>(base + inc);
+    base += sums[31];
+  }
+  if (tid == 0) w.seq_group[0] = 0;
+  __syncthreads();
+  const int groups = static_cast<int>(base);
+  int64_t tiles = 0;
+  int oob = 0;
+  for (int g0 = 0; g0 < groups; g0 += kPlanThreads) {
+    const int g = g0 + tid;
+    int64_t nt = 0;
+    if (g < groups) {
+      int lo = 0, hi = p.B - 1;   // the last sequence whose first group is at or below g
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (w.seq_group[mid] <= g) lo = mid;
+        else hi = mid - 1;
+      }
+      const int k = g - w.seq_group[lo];
+      const int q0 = p.q_seq_offsets[lo], q1 = p.q_seq_offsets[lo + 1];
+      Group gr;
+      gr.kv_row0 = p.cache_offsets[lo];
+      gr.seq_len = static_cast<int32_t>(p.cache_offsets[lo + 1] - gr.kv_row0);
+      gr.pad0 = gr.pad1 = 0;
+      if (p.k_sel >= 0) {
+        const int h0 = (k % per_tok) * kRows;
+        gr.row0 = (q0 + k / per_tok) * p.H + h0;
+        gr.nrows = p.H - h0 < kRows ? p.H - h0 : kRows;
+        gr.ntok = p.k_sel;
+      } else {
+        gr.row0 = q0 * p.H + k * kRows;
+        const int left = q1 * p.H - gr.row0;
+        gr.nrows = left < kRows ? left : kRows;
+        int top = -1;
+        for (int t = gr.row0 / p.H; t <= (gr.row0 + gr.nrows - 1) / p.H; ++t) {
+          const int pos = p.positions[t];
+          if (pos < -1 || pos >= gr.seq_len) oob = 1;
+          else top = pos > top ? pos : top;
+        }
+        gr.ntok = top + 1;
+      }
+      nt = gr.ntok > 0 ? (gr.ntok + kTile - 1) / kTile : 1;   // an empty group still writes its rows
+      w.group[g] = gr;
+    }
+    const int64_t inc = block_scan(nt, sums);
+    if (g < groups) w.tile0[g] = tiles + inc - nt;
+    tiles += sums[31];
+  }
+  if (oob) atomicOr(p.err, kErrBounds);
+  if (tid == 0) {
+    w.tile0[groups] = tiles;
+    w.plan->tiles = tiles;
+    w.plan->groups = groups;
+    w.plan->bad = 0;
+    w.plan->spoiled = 0;
   }
 }
 
-__global__ void __launch_bounds__(kWarps * 32) latent_simple_kernel(LatentArgs a, const int* bad) {
-  const int lane = threadIdx.x & 31;
-  const int64_t r = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  if (r >= static_cast<int64_t>(a.T) * a.H) return;
-  const int t = static_cast<int>(r / a.H);
-  int64_t row0 = 0, len = 0;
-  int n = 0;
-  if (!*bad) {
-    if (t < a.q_seq_offsets[0] || t >= a.q_seq_offsets[a.B]) return;   // a token of no sequence
-    int lo = 0, hi = a.B - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (a.q_seq_offsets[mid] <= t) lo = mid;
-      else hi = mid - 1;
-    }
-    row0 = a.cache_offsets[lo];
-    len = a.cache_offsets[lo + 1] - row0;
-    if (a.k_sel >= 0) {
-      n = a.k_sel;
-    } else {
-      const int p = a.positions[t];
-      if (p >= -1 && p < len) n = p + 1;
-      else if (lane == 0) atomicOr(a.err, kErrBounds);
+// The tiles [a, b) of a block's share.
+__device__ __forceinline__ void share(int64_t tiles, int block, int blocks, int64_t* a, int64_t* b) {
+  *a = tiles * block / blocks;
+  *b = tiles * (block + 1) / blocks;
+}
+
+// ---------------------------------------------------------------- pieces of PTX
+__device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t lbo, uint32_t sbo) {
+  // MN-major operand, 128-byte swizzle: 64 values along M/N per 128-byte row, `lbo` bytes to the
+  // next 64, `sbo` to the next 8 rows along K
+  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
+         (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (static_cast<uint64_t>(1) << 46) |
+         (static_cast<uint64_t>(2) << 61);
+}
+
+__device__ __forceinline__ float ex2_approx(float x) {   // relative error near 2^-22; 2^-inf = 0
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+  for (int d = 16; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
+  return v;
+}
+
+// 48 consecutive fp32 columns of the warp's TMEM lanes, and the wait for them
+__device__ __forceinline__ void tmem_ld48(uint32_t a, float (&x)[48]) {
+  uint32_t r[48];
+#pragma unroll
+  for (int i = 0; i < 3; ++i)
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(r[16 * i]), "=r"(r[16 * i + 1]), "=r"(r[16 * i + 2]), "=r"(r[16 * i + 3]), "=r"(r[16 * i + 4]),
+          "=r"(r[16 * i + 5]), "=r"(r[16 * i + 6]), "=r"(r[16 * i + 7]), "=r"(r[16 * i + 8]), "=r"(r[16 * i + 9]),
+          "=r"(r[16 * i + 10]), "=r"(r[16 * i + 11]), "=r"(r[16 * i + 12]), "=r"(r[16 * i + 13]),
+          "=r"(r[16 * i + 14]), "=r"(r[16 * i + 15])
+        : "r"(a + 16 * i)
+        : "memory");
+  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+  for (int i = 0; i < 48; ++i) asm volatile("mov.b32 %0, %1;" : "=f"(x[i]) : "r"(r[i]));
+}
+
+// ---------------------------------------------------------------- 4-bit rows
+// 64 values of a row: eight words of codes (first value in the lowest nibble) and four scales
+struct Fp4Chunk {
+  uint4 a, b;
+  uint32_t sc;
+};
+
+__device__ __forceinline__ Fp4Chunk fp4_load(const uint8_t* row, int c) {
+  Fp4Chunk f;
+  f.a = *reinterpret_cast<const uint4*>(row + 32 * c);
+  f.b = *reinterpret_cast<const uint4*>(row + 32 * c + 16);
+  f.sc = *reinterpret_cast<const uint32_t*>(row + kLatCodes + 4 * c);
+  return f;
+}
+
+// e4m3 scale as bf16 in both halves (exact: 4 significant bits)
+__device__ __forceinline__ uint32_t scale_bf16x2(uint32_t c) {
+  const uint32_t e = (c >> 3) & 15u, m = c & 7u;
+  const float v = e ? __uint_as_float(((e + 120u) << 23) | (m << 20)) : static_cast<float>(m) * 0x1p-9f;
+  return __byte_perm(__float_as_uint(v), 0, 0x3232);
+}
+
+__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+  uint32_t d;
+  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  return d;
+}
+
+// Eight codes as eight bf16 values times their scale.  The high and the low byte of a magnitude's
+// bf16 form are looked up with the three magnitude bits as byte selectors; the two sign bits of a
+// pair reach bits 15 and 31 through one multiplication (its partial products do not overlap).
+__device__ __forceinline__ uint4 fp4_word(uint32_t w, uint32_t s2) {
+  const uint32_t mag = w & 0x77777777u, sgn = w & 0x88888888u;
+  uint4 r;
+  uint32_t* const o = reinterpret_cast<uint32_t*>(&r);
+#pragma unroll
+  for (int hlf = 0; hlf < 2; ++hlf) {
+    const uint32_t sel = hlf ? mag >> 16 : mag;
+    const uint32_t hi = __byte_perm(0x3F3F3F00u, 0x40404040u, sel), lo = __byte_perm(0xC0800000u, 0xC0804000u, sel);
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t v = __byte_perm(lo, hi, k ? 0x7362 : 0x5140);
+      const uint32_t b = __byte_perm(sgn, 0, 0x4440 + 2 * hlf + k);
+      o[2 * hlf + k] = mul_bf16x2(v ^ ((b * 0x01001000u) & 0x80008000u), s2);
     }
   }
-  // lane l: latent values 16 l .. 16 l + 15 and rope values 2 l, 2 l + 1
-  const uint4* qs = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.q) + r * kLatDim);
-  float q[18], o[16];
-  {
-    const uint4 u0 = qs[2 * lane], u1 = qs[2 * lane + 1];
-    const uint32_t w[9] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w,
-                           reinterpret_cast<const uint32_t*>(qs)[kLatV / 2 + lane]};
+  return r;
+}
+
+// The chunk as a 128-byte row of a swizzled tile: 16-byte unit u of row r at unit u ^ (r & 7)
+__device__ __forceinline__ void fp4_store(uint8_t* dst_row, int r, const Fp4Chunk& f) {
+  const uint32_t w[8] = {f.a.x, f.a.y, f.a.z, f.a.w, f.b.x, f.b.y, f.b.z, f.b.w};
 #pragma unroll
-    for (int k = 0; k < 9; ++k) q[2 * k] = bf_lo(w[k]), q[2 * k + 1] = bf_hi(w[k]);
+  for (int k = 0; k < 4; ++k) {
+    const uint32_t s2 = scale_bf16x2((f.sc >> (8 * k)) & 0xFFu);
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      *reinterpret_cast<uint4*>(dst_row + (((2 * k + j) ^ (r & 7)) * 16)) = fp4_word(w[2 * k + j], s2);
   }
-#pragma unroll
-  for (int k = 0; k < 16; ++k) o[k] = 0.f;
-  float m = -INFINITY, l = 0.f;
-  for (int j = 0; j < n; ++j) {
-    int64_t pos = j;
-    if (a.k_sel >= 0) {
-      pos = a.idx[static_cast<int64_t>(t) * a.k_sel + j];
-      if (pos >= len && lane == 0) atomicOr(a.err, kErrBounds);
-      if (pos < 0 || pos >= len) continue;
+}
+
+// ---------------------------------------------------------------- attention
+struct alignas(16) Misc {
+  uint64_t full[kStages], empty[kStages], zero_req[kStages], zeroed[kStages];
+  uint64_t q_full, q_empty, s_full, s_empty, p_full, pv_done, mma_done;
+  uint32_t tmem;
+  int abort;
+  int first_group;
+  int pad;
+  alignas(16) float m[kRows];        // reference of each row (log2 units)
+  alignas(16) float f[kRows];        // factor of a raised reference; at the end 1 / sum
+  alignas(16) int limit[kRows];      // last position the row attends to
+  alignas(16) float red[kSoftWarps][48];
+  int spoiled[kRows];                // the row's sums hold a NaN that its weights do not
+};
+
+constexpr int kOffRing = kQBytes;
+constexpr int kOffP = kOffRing + kStages * kStage;
+constexpr int kOffMisc = kOffP + 2 * kPHalf;
+constexpr int kSmem = kOffMisc + static_cast<int>(sizeof(Misc)) + 1024;
+static_assert(kSmem <= 232448, "shared memory per block");
+
+// One block's walk over its pieces of groups, the same for every role.
+struct Piece {
+  Group g;
+  int gi;         // group
+  int t0, n;      // first tile inside the group, number of tiles
+  bool first, last;   // holds the group's first / last tile
+};
+
+struct Walk {
+  int64_t at, end;
+  int gi;
+  const Ws& w;
+  __device__ Walk(const Ws& ws, int64_t a, int64_t b, int g) : at(a), end(b), gi(g), w(ws) {}
+  __device__ bool next(Piece* p) {
+    if (at >= end) return false;
+    const int64_t s = w.tile0[gi], e = w.tile0[gi + 1];
+    p->g = w.group[gi];
+    p->gi = gi;
+    p->t0 = static_cast<int>(at - s);
+    const int64_t stop = e < end ? e : end;
+    p->n = static_cast<int>(stop - at);
+    p->first = at == s;
+    p->last = stop == e;
+    at = stop;
+    ++gi;
+    return true;
+  }
+};
+
+// tokens of the group that tile t holds
+__device__ __forceinline__ int tile_tokens(const Group& g, int t) {
+  const int left = g.ntok - t * kTile;
+  return left < kTile ? left : kTile;
+}
+
+template <bool FP4>
+__global__ void __launch_bounds__(kThreads, 1)
+    latent_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmC, Params p) {
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  uint8_t* const sQ = smem;
+  uint8_t* const sRing = smem + kOffRing;
+  uint8_t* const sP = smem + kOffP;
+  Misc& mi = *reinterpret_cast<Misc*>(smem + kOffMisc);
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const Ws& w = p.ws;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kStages; ++s) {
+      mbar_init(&mi.full[s], FP4 ? kFillWarps * 32 : 1);
+      mbar_init(&mi.empty[s], 1);
+      mbar_init(&mi.zero_req[s], 1);
+      mbar_init(&mi.zeroed[s], 1);
     }
-    float c[18];
-    if (a.fp4) {
-      const uint8_t* src = static_cast<const uint8_t*>(a.kv) + (row0 + pos) * kLatRow4;
-      const uint2 w = reinterpret_cast<const uint2*>(src)[lane];
-      const uint32_t sc = src[kLatCodes + lane];
-      const uint32_t e8 = (sc >> 3) & 15u;
-      const float s = e8 ? __uint_as_float(((e8 + 120u) << 23) | ((sc & 7u) << 20)) : static_cast<float>(sc & 7u) * 0x1p-9f;
-#pragma unroll
-      for (int k = 0; k < 16; ++k) {
-        const uint32_t nib = ((k < 8 ? w.x : w.y) >> (4 * (k & 7))) & 15u, e = (nib >> 1) & 3u;
-        const float mag = e ? __uint_as_float(((e + 126u) << 23) | ((nib & 1u) << 22)) : 0.5f * static_cast<float>(nib & 1u);
-        c[k] = (nib & 8u ? -mag : mag) * s;
+    mbar_init(&mi.q_full, 1);
+    mbar_init(&mi.q_empty, 1);
+    mbar_init(&mi.s_full, 1);
+    mbar_init(&mi.s_empty, kSoftWarps);
+    mbar_init(&mi.p_full, kSoftWarps);
+    mbar_init(&mi.pv_done, 1);
+    mbar_init(&mi.mma_done, 1);
+    mi.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == kMmaWarp) {
+    tmem_alloc(&mi.tmem, 512);
+    tmem_relinquish();
+  }
+  int64_t a0, a1;
+  share(w.plan->tiles, blockIdx.x, gridDim.x, &a0, &a1);
+  if (warp == 0 && a0 < a1) {
+    // the group that holds tile a0: the last whose first tile is at or below it (32 probes a step)
+    int lo = 0, n = w.plan->groups;
+    while (n > 1) {
+      const int step = (n + 31) / 32, i = lo + lane * step;
+      const unsigned in = __ballot_sync(0xffffffffu, lane * step < n && w.tile0[i] <= a0);
+      const int k = 31 - __clz(in);
+      lo += k * step;
+      n = n - k * step < step ? n - k * step : step;
+    }
+    if (lane == 0) mi.first_group = lo;
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = mi.tmem;
+  const WaitCtl wc{p.err, &mi.abort, p.timeout_ns};
+  Walk walk(w, a0, a1, mi.first_group);
+  Piece pc;
+
+  if (warp < kFillWarps) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFillRegs));
+    // ============================================================ fill
+    uint32_t it = 0;        // ring stages so far
+    uint32_t segs = 0;
+    bool ok = true;
+    if (!FP4 && warp == 2) {
+      // zero the rows of a group's last tile that its MMAs read behind its last token
+      uint32_t ph = 0;      // per-stage phase bits of zero_req
+      while (ok && walk.next(&pc)) {
+        if (pc.g.ntok == 0) continue;
+        uint32_t stages = 0;
+        for (int t = 0; t < pc.n; ++t) stages += 9 + (tile_tokens(pc.g, pc.t0 + t) > 64 ? 8 : 4);
+        const int v = tile_tokens(pc.g, pc.t0 + pc.n - 1);
+        if (pc.last && (v & 15)) {
+          const int halves = v > 64 ? 2 : 1;
+          const int r0 = v - 64 * (halves - 1), r1 = (r0 + 15) & ~15;
+          for (int j = 0; j < 4 && ok; ++j) {
+            const uint32_t at = it + stages - 4 * halves + j * halves + (halves - 1), s = at % kStages;
+            ok = mbar_wait(&mi.zero_req[s], (ph >> s) & 1, wc) && mbar_wait(&mi.full[s], (at / kStages) & 1, wc);
+            if (!ok) break;
+            ph ^= 1u << s;
+            for (int u = lane; u < (r1 - r0) * 16; u += 32) {
+              const int r = r0 + (u >> 4), un = u & 15;
+              *reinterpret_cast<uint4*>(sRing + s * kStage + (un >> 3) * 8192 + r * 128 + (un & 7) * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&mi.zeroed[s]);
+          }
+        }
+        it += stages;
       }
-      const uint32_t rp = reinterpret_cast<const uint32_t*>(src + kLatCodes + kLatScales)[lane];
-      c[16] = bf_lo(rp), c[17] = bf_hi(rp);
-    } else {
-      const uint4* src = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(a.kv) + (row0 + pos) * kLatDim);
-      const uint4 u0 = src[2 * lane], u1 = src[2 * lane + 1];
-      const uint32_t w[9] = {u0.x, u0.y, u0.z, u0.w, u1.x, u1.y, u1.z, u1.w,
-                             reinterpret_cast<const uint32_t*>(src)[kLatV / 2 + lane]};
+    } else if (FP4 || (warp == 0 && lane == 0)) {
+      const int i = threadIdx.x;       // FP4: token of the tile (scores), token and half (values)
+      auto q_load = [&]() {
+        if (segs > 0 && !mbar_wait(&mi.q_empty, (segs - 1) & 1, wc)) return false;
+        mbar_arrive_expect_tx(&mi.q_full, kQBytes);
+        for (int c = 0; c < 9; ++c) tma_load_2d(sQ + c * kQChunk, &tmQ, &mi.q_full, 64 * c, pc.g.row0);
+        return true;
+      };
+      auto acquire = [&](uint32_t s) { return it < kStages || mbar_wait(&mi.empty[s], (it / kStages - 1) & 1, wc); };
+      while (ok && walk.next(&pc)) {
+        if (pc.g.ntok == 0) continue;
+        if (!FP4 || i == 0) ok = q_load();
+        ++segs;
+        if constexpr (FP4) {
+          const uint8_t* const base = p.kv4 + pc.g.kv_row0 * kLatRow4;
+          const int32_t* const sel =
+              p.k_sel >= 0 ? p.idx + static_cast<int64_t>(pc.g.row0 / p.H) * p.k_sel : nullptr;
+          // cache row of token j of tile t, or null
+          auto row_of = [&](int t, int j) -> const uint8_t* {
+            const int k = t * kTile + j;
+            if (k >= pc.g.ntok) return nullptr;
+            int pos = k;
+            if (sel) {
+              pos = sel[k];
+              if (pos >= pc.g.seq_len) atomicOr(p.err, kErrBounds);
+              if (pos < 0 || pos >= pc.g.seq_len) return nullptr;
+            }
+            return base + static_cast<int64_t>(pos) * kLatRow4;
+          };
+          auto prefetch = [&](int t) {
+            if (t >= pc.t0 + pc.n) return;
+            const uint8_t* r = row_of(t, i);
+            if (!r) return;
 #pragma unroll
-      for (int k = 0; k < 9; ++k) c[2 * k] = bf_lo(w[k]), c[2 * k + 1] = bf_hi(w[k]);
+            for (int k = 0; k < 4; ++k) asm volatile("prefetch.global.L2 [%0];" ::"l"(r + 128 * k));
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(r + kLatRow4 - 16));
+          };
+          auto values = [&](int t) {
+            const int v = tile_tokens(pc.g, t);
+            const int halves = v > 64 ? 2 : 1;
+            const int j = i & 63, sub = i >> 6;
+            const uint8_t* r[2] = {row_of(t, j), halves == 2 ? row_of(t, 64 + j) : nullptr};
+            Fp4Chunk nx = {};
+            if (r[0]) nx = fp4_load(r[0], sub);
+            for (int k = 0; k < 4 * halves; ++k) {
+              const int hf = halves == 2 ? k & 1 : 0;
+              const Fp4Chunk cur = nx;
+              const bool have = r[hf] != nullptr;
+              if (k + 1 < 4 * halves) {
+                const int hn = halves == 2 ? (k + 1) & 1 : 0, blk = halves == 2 ? (k + 1) >> 1 : k + 1;
+                if (r[hn]) nx = fp4_load(r[hn], 2 * blk + sub);
+              }
+              const uint32_t s = it % kStages;
+              if (!acquire(s)) return false;
+              uint8_t* const dst = sRing + s * kStage + sub * 8192 + j * 128;
+              if (have) {
+                fp4_store(dst, j, cur);
+              } else {
+#pragma unroll
+                for (int u = 0; u < 8; ++u) reinterpret_cast<uint4*>(dst)[u] = make_uint4(0u, 0u, 0u, 0u);
+              }
+              fence_proxy_async_smem();
+              mbar_arrive(&mi.full[s]);
+              ++it;
+            }
+            return true;
+          };
+          prefetch(pc.t0);
+          for (int t = pc.t0; t < pc.t0 + pc.n && ok; ++t) {
+            prefetch(t + 1);
+            const uint8_t* r = row_of(t, i);
+            Fp4Chunk nx = {};
+            if (r) nx = fp4_load(r, 0);
+            for (int c = 0; c < 9; ++c) {
+              const Fp4Chunk cur = nx;
+              if (r && c + 1 < 8) nx = fp4_load(r, c + 1);
+              const uint32_t s = it % kStages;
+              if (!(ok = acquire(s))) break;
+              uint8_t* const dst = sRing + s * kStage + i * 128;
+              if (r && c < 8) {
+                fp4_store(dst, i, cur);
+              } else if (r) {
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                  *reinterpret_cast<uint4*>(dst + ((u ^ (i & 7)) * 16)) =
+                      reinterpret_cast<const uint4*>(r + kLatCodes + kLatScales)[u];
+              }   // a missing token's score is masked, whatever its row holds
+              fence_proxy_async_smem();
+              mbar_arrive(&mi.full[s]);
+              ++it;
+            }
+            if (ok && t > pc.t0) ok = values(t - 1);
+          }
+          if (ok) ok = values(pc.t0 + pc.n - 1);
+        } else {
+          auto load = [&](int x0, int x1, int y0, int y1, bool two, bool zero) {
+            const uint32_t s = it % kStages;
+            if (!acquire(s)) return false;
+            mbar_arrive_expect_tx(&mi.full[s], two ? kStage : kStage / 2);
+            tma_load_2d(sRing + s * kStage, &tmC, &mi.full[s], x0, y0);
+            if (two) tma_load_2d(sRing + s * kStage + kStage / 2, &tmC, &mi.full[s], x1, y1);
+            if (zero) mbar_arrive(&mi.zero_req[s]);
+            ++it;
+            return true;
+          };
+          const int y = static_cast<int>(pc.g.kv_row0);
+          auto values = [&](int t) {
+            const int v = tile_tokens(pc.g, t), halves = v > 64 ? 2 : 1;
+            for (int j = 0; j < 4; ++j)
+              for (int hf = 0; hf < halves; ++hf) {
+                const int yy = y + t * kTile + 64 * hf;
+                if (!load(128 * j, 128 * j + 64, yy, yy, true, hf == halves - 1 && (v & 15))) return false;
+              }
+            return true;
+          };
+          for (int t = pc.t0; t < pc.t0 + pc.n && ok; ++t) {
+            const bool two = tile_tokens(pc.g, t) > 64;
+            const int yy = y + t * kTile;
+            for (int c = 0; c < 9 && ok; ++c) ok = load(64 * c, 64 * c, yy, yy + 64, two, false);
+            if (ok && t > pc.t0) ok = values(t - 1);
+          }
+          if (ok) ok = values(pc.t0 + pc.n - 1);
+        }
+      }
+      if (!FP4 || i == 0) {
+        // on an early exit the loads in flight land before the block ends
+        if (!ok) {
+          auto drain = [&](uint64_t* bar, uint32_t parity) {
+            const uint64_t t0 = global_timer_ns();
+            while (!mbar_try_wait(smem_u32(bar), parity) && global_timer_ns() - t0 <= kDrainNs) {
+            }
+          };
+          if (!FP4)
+            for (uint32_t k = it > kStages ? it - kStages : 0; k < it; ++k) drain(&mi.full[k % kStages], (k / kStages) & 1);
+          if (segs > 0) drain(&mi.q_full, (segs - 1) & 1);
+        }
+      }
     }
-    float x = 0.f;
+  } else if (warp < kMmaWarp) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    // ============================================================ softmax
+    const int wg = (warp - kFillWarps) >> 2, qd = warp & 3;
+    const int tok = qd * 32 + lane;                       // token of the tile, TMEM lane
+    const uint32_t tlane = tmem + (static_cast<uint32_t>(qd * 32) << 16);
+    const int wtid = (warp - kFillWarps - 4 * wg) * 32 + lane;
+    const int bar_id = 1 + wg;
+    uint32_t done = 0;      // tiles so far
+    // A wait that ran out is skipped from then on, but the walk goes on to its end: the warps of
+    // a half meet at named barriers and none may leave the others there.  The results are then
+    // worthless, and the error word says so.
+    bool ok = true;
+    while (walk.next(&pc)) {
+      const Group& g = pc.g;
+      // columns (rows of the group) of this half: the N of the MMAs split into two runs of 16s
+      const int n16 = (g.nrows + 15) / 16, c0 = wg ? (n16 + 1) / 2 * 16 : 0;
+      const int nc = wg ? n16 * 16 - c0 : (n16 + 1) / 2 * 16;
+      // rows' references and limits
+      int lim = -1;
+      if (wtid < nc) {
+        const int r = c0 + wtid;
+        if (p.k_sel >= 0) {
+          lim = 0;
+        } else if (r < g.nrows) {
+          lim = p.positions[(g.row0 + r) / p.H];
+          if (lim >= g.seq_len || lim < -1) lim = -1;
+        }
+        mi.m[r] = kUnset;
+        mi.limit[r] = lim;
+        mi.spoiled[r] = 0;
+      }
+      // padding rows (r >= nrows) ask for nothing and may be masked or not
+      const int mine = wtid < nc && c0 + wtid < g.nrows ? lim : 0x7FFFFFFF;
+      int low = __reduce_min_sync(0xffffffffu, mine);
+      if (lane == 0) mi.red[warp - kFillWarps][0] = __int_as_float(low);
+      named_bar_sync(bar_id, 128);
+      for (int k = 0; k < 4; ++k) {
+        const int o = __float_as_int(mi.red[4 * wg + k][0]);
+        low = o < low ? o : low;
+      }
+      named_bar_sync(bar_id, 128);
+      float l[48];
 #pragma unroll
-    for (int k = 0; k < 18; ++k) x = fmaf(q[k], c[k], x);
+      for (int c = 0; c < 48; ++c) l[c] = 0.f;
+      const int32_t* const sel = p.k_sel >= 0 ? p.idx + static_cast<int64_t>(g.row0 / p.H) * p.k_sel : nullptr;
+
+      for (int t = 0; g.ntok > 0 && t < pc.n; ++t, ++done) {
+        const int first_pos = (pc.t0 + t) * kTile;
+        int pos = first_pos + tok;
+        bool masked = sel || first_pos + kTile - 1 > low;
+        if (sel) {
+          const int e = pos < g.ntok ? sel[pos] : -1;
+          pos = e >= 0 && e < g.seq_len ? 0 : 0x7FFFFFFF;
+        }
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(&mi.s_full, done & 1, wc));
+        tc_fence_after();
+        float x[48];
+        tmem_ld48(tlane + kTmemS + c0, x);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&mi.s_empty);
+        const float4* const m4 = reinterpret_cast<const float4*>(mi.m + c0);
+        if (masked) {
+          const int4* const l4 = reinterpret_cast<const int4*>(mi.limit + c0);
 #pragma unroll
-    for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-    x *= a.scale;
-    const float mn = fmaxf(m, x);
-    const float f = m == -INFINITY ? 0.f : __expf(m - mn);
-    const float p = x == -INFINITY ? 0.f : __expf(x - mn);
-    l = l * f + p;
+          for (int c = 0; c < 12; ++c) {
+            if (4 * c < nc) {
+              const int4 v = l4[c];
+              x[4 * c] = pos <= v.x ? x[4 * c] : -INFINITY;
+              x[4 * c + 1] = pos <= v.y ? x[4 * c + 1] : -INFINITY;
+              x[4 * c + 2] = pos <= v.z ? x[4 * c + 2] : -INFINITY;
+              x[4 * c + 3] = pos <= v.w ? x[4 * c + 3] : -INFINITY;
+            }
+          }
+        }
+        float top = -INFINITY;
 #pragma unroll
-    for (int k = 0; k < 16; ++k) o[k] = fmaf(o[k], f, p * c[k]);
-    m = mn;
+        for (int c = 0; c < 12; ++c) {
+          if (4 * c < nc) {
+            const float4 m = m4[c];
+            top = fmaxf(top, fmaf(x[4 * c], p.scale_log2, -m.x));
+            top = fmaxf(top, fmaf(x[4 * c + 1], p.scale_log2, -m.y));
+            top = fmaxf(top, fmaf(x[4 * c + 2], p.scale_log2, -m.z));
+            top = fmaxf(top, fmaf(x[4 * c + 3], p.scale_log2, -m.w));
+          }
+        }
+        if (named_bar_or(bar_id, 128, top > 8.f)) {
+          // some row's reference rises: the tile's maximum of every row, over the tokens
+#pragma unroll
+          for (int c = 0; c < 48; ++c) {
+            if (c < nc) {
+              const float v = warp_max(x[c]);
+              if (lane == (c & 31)) mi.red[warp - kFillWarps][c] = v;
+            }
+          }
+          named_bar_sync(bar_id, 128);
+          if (wtid < nc) {
+            float v = -INFINITY;
+            for (int k = 0; k < 4; ++k) v = fmaxf(v, mi.red[4 * wg + k][wtid]);
+            v *= p.scale_log2;
+            const float old = mi.m[c0 + wtid];
+            const float now = v > old + 8.f ? v : old;
+            mi.m[c0 + wtid] = now;
+            mi.f[c0 + wtid] = ex2_approx(old - now);
+          }
+          named_bar_sync(bar_id, 128);
+          const float4* const f4 = reinterpret_cast<const float4*>(mi.f + c0);
+#pragma unroll
+          for (int c = 0; c < 12; ++c) {
+            if (4 * c < nc) {
+              const float4 f = f4[c];
+              l[4 * c] *= f.x;
+              l[4 * c + 1] *= f.y;
+              l[4 * c + 2] *= f.z;
+              l[4 * c + 3] *= f.w;
+            }
+          }
+          if (t > 0) {
+            // the sums so far, once every earlier product has landed in them
+            ok = ok && __all_sync(0xffffffffu, mbar_wait(&mi.pv_done, (done - 1) & 1, wc));
+            tc_fence_after();
+#pragma unroll 1
+            for (int j = 0; j < 4; ++j) {
+#pragma unroll 1
+              for (int cc = 0; cc < nc; cc += 16) {
+                uint32_t o[16];
+                const uint32_t a = tlane + j * kRows + c0 + cc;
+                asm volatile(
+                    "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+                    "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+                    "tcgen05.wait::ld.sync.aligned;"
+                    : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7]),
+                      "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]), "=r"(o[14]),
+                      "=r"(o[15])
+                    : "r"(a)
+                    : "memory");
+#pragma unroll
+                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * mi.f[c0 + cc + k]);
+                asm volatile(
+                    "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+                    "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};\n\t"
+                    "tcgen05.wait::st.sync.aligned;"
+                    ::"r"(a), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7]),
+                      "r"(o[8]), "r"(o[9]), "r"(o[10]), "r"(o[11]), "r"(o[12]), "r"(o[13]), "r"(o[14]), "r"(o[15])
+                    : "memory");
+              }
+            }
+          }
+        }
+        // weights: 2^(x - m), summed before their rounding to bf16 (lse keeps fp32's precision;
+        // out gets one rounding of up to 2^-8 a weight, the operand type of the product)
+        uint32_t pk[24];
+#pragma unroll
+        for (int c = 0; c < 12; ++c) {
+          if (4 * c < nc) {
+            const float4 m = m4[c];
+            const float e0 = ex2_approx(fmaf(x[4 * c], p.scale_log2, -m.x));
+            const float e1 = ex2_approx(fmaf(x[4 * c + 1], p.scale_log2, -m.y));
+            const float e2 = ex2_approx(fmaf(x[4 * c + 2], p.scale_log2, -m.z));
+            const float e3 = ex2_approx(fmaf(x[4 * c + 3], p.scale_log2, -m.w));
+            l[4 * c] += e0;
+            l[4 * c + 1] += e1;
+            l[4 * c + 2] += e2;
+            l[4 * c + 3] += e3;
+            pk[2 * c] = pack2(e0, e1);
+            pk[2 * c + 1] = pack2(e2, e3);
+          }
+        }
+        // the weights' place in shared memory is free once the previous tile's product is done
+        if (done > 0) ok = ok && __all_sync(0xffffffffu, mbar_wait(&mi.pv_done, (done - 1) & 1, wc));
+#pragma unroll
+        for (int u = 0; u < 6; ++u) {
+          if (8 * u < nc) {
+            const int col = c0 + 8 * u;
+            *reinterpret_cast<uint4*>(sP + (col >> 6) * kPHalf + tok * 128 + ((((col & 63) >> 3) ^ (tok & 7)) * 16)) =
+                make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
+          }
+        }
+        fence_proxy_async_smem();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&mi.p_full);
+      }
+      // the rows' sums over the 128 threads
+      named_bar_sync(bar_id, 128);
+#pragma unroll
+      for (int c = 0; c < 48; ++c) {
+        if (c < nc) {
+          float v = l[c];
+#pragma unroll
+          for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
+          if (lane == (c & 31)) mi.red[warp - kFillWarps][c] = v;
+        }
+      }
+      named_bar_sync(bar_id, 128);
+      const bool whole = pc.first && pc.last;
+      const int slot = 2 * blockIdx.x + (pc.first ? 1 : 0);     // head pieces 0, tail pieces 1
+      if (wtid < nc) {
+        float sum = 0.f;
+        for (int k = 0; k < 4; ++k) sum += mi.red[4 * wg + k][wtid];
+        const int r = c0 + wtid;
+        mi.f[r] = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+        if (r < g.nrows) {
+          const float m = mi.m[r];
+          if (whole) p.lse[g.row0 + r] = sum == 0.f ? -INFINITY : fmaf(m, 0.69314718055994531f, logf(sum));
+          else w.ml[static_cast<int64_t>(slot) * kRows + r] = make_float2(m, sum);
+        }
+      }
+      named_bar_sync(bar_id, 128);
+      if (g.ntok > 0) {
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(&mi.pv_done, (done - 1) & 1, wc));
+        tc_fence_after();
+      }
+#pragma unroll 1
+      for (int j = 0; j < 4; ++j) {
+        float o[48];
+        if (g.ntok > 0) tmem_ld48(tlane + j * kRows + c0, o);
+        const int dim = 128 * j + tok;
+        if (whole) {
+          __nv_bfloat16* const ob = p.out + static_cast<int64_t>(g.row0 + c0) * kLatV + (dim & ~1);
+#pragma unroll
+          for (int c = 0; c < 48; c += 2) {
+            if (c < nc) {
+              // even lanes keep row c, odd lanes row c + 1, each with its pair of dims
+              const float i0 = mi.f[c0 + c], i1 = mi.f[c0 + c + 1];
+              const float v0 = i0 != 0.f ? o[c] * i0 : 0.f, v1 = i1 != 0.f ? o[c + 1] * i1 : 0.f;
+              if (!FP4) {
+                if (v0 != v0 && i0 == i0) mi.spoiled[c0 + c] = 1;
+                if (v1 != v1 && i1 == i1) mi.spoiled[c0 + c + 1] = 1;
+              }
+              const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? v0 : v1, 1);
+              const uint32_t pr = lane & 1 ? pack2(got, v1) : pack2(v0, got);
+              const int r = c + (lane & 1);
+              if (c0 + r < g.nrows) *reinterpret_cast<uint32_t*>(ob + static_cast<int64_t>(r) * kLatV) = pr;
+            }
+          }
+        } else {
+          float* const ob = w.o + slot * kSlotFloats + static_cast<int64_t>(c0) * kLatV + dim;
+#pragma unroll
+          for (int c = 0; c < 48; ++c)
+            if (c < nc && c0 + c < g.nrows) ob[c * kLatV] = o[c];
+        }
+      }
+      tc_fence_before();
+      named_bar_sync(bar_id, 128);   // f, m and red are free for the next piece
+      if (!FP4 && whole && wtid < nc && c0 + wtid < g.nrows && mi.spoiled[c0 + wtid])
+        w.spoiled[atomicAdd(&w.plan->spoiled, 1)] = g.row0 + c0 + wtid;
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
+    // ============================================================ MMA issuer
+    if (warp == kMmaWarp && lane == 0) {
+    uint32_t it = 0, done = 0, segs = 0, zph = 0;
+    bool ok = true;
+    const uint32_t qa = smem_u32(sQ), ra = smem_u32(sRing), pa = smem_u32(sP);
+    while (ok && walk.next(&pc)) {
+      const Group& g = pc.g;
+      if (g.ntok == 0) continue;
+      const int N = (g.nrows + 15) / 16 * 16;
+      const uint32_t idesc_s = umma_idesc_bf16(128, N);
+      const uint32_t idesc_o = idesc_s | (1u << 15) | (1u << 16);   // both operands MN-major
+      if (!(ok = mbar_wait(&mi.q_full, segs & 1, wc))) break;
+      ++segs;
+      // O^T += C_latent^T . P^T of the tile `u` of the piece
+      auto values = [&](int u) {
+        const int v = tile_tokens(g, pc.t0 + u), halves = v > 64 ? 2 : 1;
+        const bool zero = !FP4 && pc.last && u == pc.n - 1 && (v & 15);
+        if (!mbar_wait(&mi.p_full, (done - (pc.n - u)) & 1, wc)) return false;
+        for (int j = 0; j < 4; ++j) {
+          for (int hf = 0; hf < halves; ++hf) {
+            const uint32_t s = it % kStages;
+            if (zero && hf == halves - 1) {
+              if (!mbar_wait(&mi.zeroed[s], (zph >> s) & 1, wc)) return false;
+              zph ^= 1u << s;
+            }
+            if (!mbar_wait(&mi.full[s], (it / kStages) & 1, wc)) return false;
+            tc_fence_after();
+            const int left = v - 64 * hf, steps = left >= 64 ? 4 : (left + 15) / 16;
+            for (int k = 0; k < steps; ++k)
+              umma_bf16(tmem + j * kRows, desc_mn(ra + s * kStage + k * 2048, 8192, 1024),
+                        desc_mn(pa + hf * 8192 + k * 2048, kPHalf, 1024), idesc_o, (u | hf | k) != 0);
+            umma_commit(&mi.empty[s]);
+            ++it;
+          }
+        }
+        umma_commit(&mi.pv_done);
+        return true;
+      };
+      done += pc.n;
+      for (int t = 0; t < pc.n && ok; ++t) {
+        const uint32_t nth = done - pc.n + t;
+        if (nth > 0 && !(ok = mbar_wait(&mi.s_empty, (nth - 1) & 1, wc))) break;
+        for (int c = 0; c < 9; ++c) {
+          const uint32_t s = it % kStages;
+          if (!(ok = mbar_wait(&mi.full[s], (it / kStages) & 1, wc))) break;
+          tc_fence_after();
+          const uint64_t ad = umma_desc_sw128(ra + s * kStage), bd = umma_desc_sw128(qa + c * kQChunk);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) umma_bf16(tmem + kTmemS, ad + 2 * k, bd + 2 * k, idesc_s, (c | k) != 0);
+          umma_commit(&mi.empty[s]);
+          ++it;
+        }
+        if (!ok) break;
+        umma_commit(&mi.s_full);
+        if (t == pc.n - 1) umma_commit(&mi.q_empty);
+        if (t > 0) ok = values(t - 1);
+      }
+      if (ok) ok = values(pc.n - 1);
+    }
+    // every MMA has finished before TMEM is freed, on an early exit too (bounded)
+    umma_commit(&mi.mma_done);
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(smem_u32(&mi.mma_done), 0) && global_timer_ns() - t0 <= kDrainNs) {
+    }
+    }
+    __syncwarp();
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  uint32_t w[8];
-#pragma unroll
-  for (int k = 0; k < 8; ++k) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(o[2 * k] * inv, o[2 * k + 1] * inv);
-    w[k] = *reinterpret_cast<const uint32_t*>(&b);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
   }
-  uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + r * kLatV);
-  dst[2 * lane] = make_uint4(w[0], w[1], w[2], w[3]);
-  dst[2 * lane + 1] = make_uint4(w[4], w[5], w[6], w[7]);
-  if (lane == 0) a.lse[r] = l > 0.f ? m + logf(l) : -INFINITY;
+}
+
+// ---------------------------------------------------------------- merge
+// Block (i, r): row r of the group that block i's share leaves unfinished, from its pieces in
+// the order of their tiles; with malformed offsets, rows of the call as attending to nothing.
+constexpr int kMergeThreads = 128;
+
+// Row `row` of out from its own prefix alone, by the block: scores of 128 tokens at a time, a
+// thread each, then four of the 512 dims a thread.  For rows that a NaN or an infinity beside
+// their prefix spoiled; lse is right already.
+__device__ void redo_row(const Params& p, int64_t row) {
+  __shared__ float sw[kMergeThreads];
+  const int tid = threadIdx.x, t = static_cast<int>(row / p.H);
+  int lo = 0, hi = p.B - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (p.q_seq_offsets[mid] <= t) lo = mid;
+    else hi = mid - 1;
+  }
+  const __nv_bfloat16* const kv = p.kv + p.cache_offsets[lo] * kLatDim;
+  const __nv_bfloat16* const q = p.q + row * kLatDim;
+  const int n = p.positions[t] + 1;
+  float m = -INFINITY, l = 0.f;
+  float o[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int s0 = 0; s0 < n; s0 += kMergeThreads) {
+    float x = -INFINITY;
+    if (s0 + tid < n) {
+      x = 0.f;
+      const __nv_bfloat16* const c = kv + static_cast<int64_t>(s0 + tid) * kLatDim;
+      for (int d = 0; d < kLatDim; ++d) x = fmaf(__bfloat162float(q[d]), __bfloat162float(c[d]), x);
+      x *= p.scale_log2;
+    }
+    __syncthreads();
+    sw[tid] = x;
+    __syncthreads();
+    float top = m;
+    for (int j = 0; j < kMergeThreads; ++j) top = fmaxf(top, sw[j]);
+    const float f = m == -INFINITY ? 0.f : ex2_approx(m - top);
+    l *= f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[k] *= f;
+    m = top;
+    const int left = n - s0 < kMergeThreads ? n - s0 : kMergeThreads;
+    for (int j = 0; j < left; ++j) {
+      const float w = m == -INFINITY ? 0.f : ex2_approx(sw[j] - m);
+      l += w;
+      const __nv_bfloat16* const c = kv + static_cast<int64_t>(s0 + j) * kLatDim + 4 * tid;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) o[k] = fmaf(w, __bfloat162float(c[k]), o[k]);
+    }
+  }
+  const float inv = l != 0.f ? 1.f / l : 0.f;
+  reinterpret_cast<uint2*>(p.out + row * kLatV)[tid] = make_uint2(pack2(o[0] * inv, o[1] * inv), pack2(o[2] * inv, o[3] * inv));
+}
+
+__global__ void __launch_bounds__(kMergeThreads) latent_merge_kernel(Params p, int blocks) {
+  const Ws& w = p.ws;
+  const int tid = threadIdx.x;
+  if (w.plan->bad) {
+    const int64_t rows = static_cast<int64_t>(p.T) * p.H;
+    const int64_t nb = static_cast<int64_t>(gridDim.x) * gridDim.y;
+    for (int64_t r = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x; r < rows; r += nb) {
+      reinterpret_cast<uint2*>(p.out + r * kLatV)[tid] = make_uint2(0u, 0u);
+      if (tid == 0) p.lse[r] = -INFINITY;
+    }
+    return;
+  }
+  {
+    const int64_t nb = static_cast<int64_t>(gridDim.x) * gridDim.y;
+    for (int64_t k = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x; k < w.plan->spoiled; k += nb)
+      redo_row(p, w.spoiled[k]);
+  }
+  const int i = blockIdx.x;
+  int64_t a, b;
+  share(w.plan->tiles, i, blocks, &a, &b);
+  if (a >= b) return;
+  // the last group of the share, if it starts in it and goes on behind it
+  int lo = 0, hi = w.plan->groups - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (w.tile0[mid] < b) lo = mid;
+    else hi = mid - 1;
+  }
+  const int64_t end = w.tile0[lo + 1];
+  if (end <= b || w.tile0[lo] < a) return;
+  const Group g = w.group[lo];
+  const int r = blockIdx.y;
+  if (r >= g.nrows) return;
+  int last = i;      // the block that holds the group's last tile
+  {
+    int l2 = i, h2 = blocks - 1;
+    while (l2 < h2) {
+      const int mid = (l2 + h2) >> 1;
+      int64_t x, y;
+      share(w.plan->tiles, mid, blocks, &x, &y);
+      if (y >= end) h2 = mid;
+      else l2 = mid + 1;
+    }
+    last = l2;
+  }
+  // pieces: the tail slot of block i, then the head slots of the blocks up to `last` (a block
+  // without tiles, between shares, has none: its m and l are skipped by its empty share)
+  float m = kUnset;
+  for (int k = i; k <= last; ++k) {
+    int64_t x, y;
+    share(w.plan->tiles, k, blocks, &x, &y);
+    if (x >= y) continue;
+    const float2 v = w.ml[static_cast<int64_t>(2 * k + (k == i)) * kRows + r];
+    if (v.y != 0.f) m = fmaxf(m, v.x);
+  }
+  float l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int k = i; k <= last; ++k) {
+    int64_t x, y;
+    share(w.plan->tiles, k, blocks, &x, &y);
+    if (x >= y) continue;
+    const int64_t slot = 2 * k + (k == i);
+    const float2 v = w.ml[slot * kRows + r];
+    const float4 c = reinterpret_cast<const float4*>(w.o + slot * kSlotFloats + static_cast<int64_t>(r) * kLatV)[tid];
+    if (v.y != 0.f) {
+      const float f = ex2_approx(v.x - m);
+      l = fmaf(v.y, f, l);
+      o.x = fmaf(c.x, f, o.x);
+      o.y = fmaf(c.y, f, o.y);
+      o.z = fmaf(c.z, f, o.z);
+      o.w = fmaf(c.w, f, o.w);
+    }
+  }
+  const float inv = l != 0.f ? 1.f / l : 0.f;
+  const int64_t row = g.row0 + r;
+  reinterpret_cast<uint2*>(p.out + row * kLatV)[tid] =
+      l != 0.f ? make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv)) : make_uint2(0u, 0u);
+  if (tid == 0) p.lse[row] = l != 0.f ? fmaf(m, 0.69314718055994531f, logf(l)) : -INFINITY;
+  if (p.kv && __syncthreads_or(l == l && l != 0.f && !(o.x == o.x && o.y == o.y && o.z == o.z && o.w == o.w))) redo_row(p, row);
 }
 
 }  // namespace
 
-int64_t latent_workspace_bytes(int64_t, int64_t, int64_t, int) { return 16; }
+int64_t latent_workspace_bytes(int64_t T, int64_t B, int64_t H, int num_sms) {
+  return carve(nullptr, T, B, H, num_sms).bytes;
+}
 
-cudaError_t launch_latent_attention(const LatentArgs& a, cudaStream_t s) {
+cudaError_t launch_latent_attention(const LatentArgs& a, const CUtensorMap& tmQ, const CUtensorMap& tmC, cudaStream_t s) {
   if (a.T == 0) return cudaSuccess;
-  int* bad = static_cast<int*>(a.workspace);
-  check_offsets_kernel<<<1, 256, 0, s>>>(a, bad);
-  const int64_t rows = static_cast<int64_t>(a.T) * a.H;
-  latent_simple_kernel<<<static_cast<unsigned>((rows + kWarps - 1) / kWarps), kWarps * 32, 0, s>>>(a, bad);
+  const int blocks = a.num_sms;
+  Params p;
+  p.T = a.T;
+  p.B = a.B;
+  p.H = a.H;
+  p.k_sel = a.k_sel;
+  p.cache_rows = a.cache_rows;
+  p.q = static_cast<const __nv_bfloat16*>(a.q);
+  p.kv = a.fp4 ? nullptr : static_cast<const __nv_bfloat16*>(a.kv);
+  p.kv4 = a.fp4 ? static_cast<const uint8_t*>(a.kv) : nullptr;
+  p.positions = a.positions;
+  p.q_seq_offsets = a.q_seq_offsets;
+  p.cache_offsets = a.cache_offsets;
+  p.idx = a.idx;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.out = static_cast<__nv_bfloat16*>(a.out);
+  p.lse = a.lse;
+  p.ws = carve(a.workspace, a.T, a.B, a.H, blocks);
+  p.err = a.err;
+  p.timeout_ns = a.timeout_ns;
+  auto kern = a.fp4 ? latent_attention_kernel<true> : latent_attention_kernel<false>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  latent_plan_kernel<<<1, kPlanThreads, 0, s>>>(p);
+  kern<<<blocks, kThreads, kSmem, s>>>(tmQ, tmC, p);
+  latent_merge_kernel<<<dim3(blocks, kRows), kMergeThreads, 0, s>>>(p, blocks);
   return cudaGetLastError();
 }
 

@@ -213,6 +213,22 @@ def test_what_lies_behind_the_prefix_is_never_used(dsa, ix):
         np.testing.assert_array_equal(got[1], want[1])
 
 
+@pytest.mark.parametrize("v", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("n,H", [(200, 40), (3000, 6)])     # in one block's share; split over many
+def test_a_row_that_only_later_queries_see_may_hold_anything(dsa, ix, v, n, H):
+    b = Batch(15, [n], [3], H)
+    b.pos = torch.tensor([n - 60, n - 20, n - 2], dtype=torch.int32)
+    want = _run(dsa, ix, b)
+    b.kv[n - 30, 5] = v
+    b.kv[n - 10] = v
+    o, lse = _run(dsa, ix, b)
+    np.testing.assert_array_equal(lse[0], want[1][0])
+    keep = Batch(15, [n], [1], H)
+    keep.q, keep.kv, keep.pos = b.q[:1], torch.nan_to_num(b.kv, 0, 0, 0), b.pos[:1]
+    _check(o[:1], lse[:1], f64(keep.q), f64(keep.kv), keep.pos.numpy(), keep.qo.numpy(), keep.co.numpy())
+    assert not np.any(np.isfinite(o[1:, :, 5]))       # they attend to it
+
+
 def test_padded_batch_leaves_its_rows_as_they_were(dsa, ix):
     b = Batch(10, [300, 100], [3, 2], 32)
     b.qo = torch.tensor([0, 2, 3], dtype=torch.int32)            # tokens 3 and 4 belong to no sequence
