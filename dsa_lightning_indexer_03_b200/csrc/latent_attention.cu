@@ -17,15 +17,15 @@
 // as eight 64-token x 128-dim pieces for its values, since Q and a whole 144 KB tile do not fit
 // together.
 //
-// latent_attention_kernel: persistent, one block of 16 warps per SM.
+// latent_attention_kernel: persistent, one block of 20 warps per SM.
 //   warps 0-3   fill the ring: one thread with TMA (bf16), or all by converting 4-bit rows; for
 //               bf16 warp 2 zeroes the rows behind a sequence's last token (0 * NaN is NaN).
-//   warps 4-11  softmax: a thread per token, half of the rows each.  The reference m of a row
+//   warps 4-15  softmax: a thread per token, a third of the rows each.  The reference m of a row
 //               is its running maximum, raised only when a score exceeds it by more than 8 (log2
 //               units, so weights stay below 256): most tiles then need no maximum over the
 //               tokens, which lie across threads, only a vote.  Sums are kept per thread and
 //               added up at the end.  Weights go to shared memory as bf16 (the MMA's operand).
-//   warp 12     (of a warpgroup that otherwise idles) issues the MMAs: S(t+1) before the values of t, so that the softmax of a tile
+//   warp 16     (of a warpgroup that otherwise idles) issues the MMAs: S(t+1) before the values of t, so that the softmax of a tile
 //               runs under the MMAs of its neighbours.
 // Work: plan_kernel lists the groups and their tiles; the blocks take equal shares of all tiles
 // in order, so a share may begin or end inside a group; such pieces leave unnormalised fp32
@@ -47,12 +47,21 @@ constexpr int kRows = 96;                    // rows (token, head) of a group
 constexpr int kTile = 128;                   // tokens of a tile
 constexpr int kQChunk = kRows * 128;         // 64 values of each row of Q
 constexpr int kQBytes = 9 * kQChunk;
-constexpr int kStages = 5;
+constexpr int kSStages = 3, kVStages = 2;    // stages of the two rings: scores, values
 constexpr int kStage = 16384;
 constexpr int kPHalf = kTile * 128;          // weights of 64 rows: 128 tokens x 128 B
-constexpr int kFillWarps = 4, kSoftWarps = 8, kMmaWarp = 12, kThreads = 16 * 32;
-// registers a thread: 128 at launch, then 96 (fill), 184 (softmax), 48 (MMA): 4 * 96 + 8 * 184 + 4 * 48 = 16 * 128
-constexpr int kFillRegs = 96, kSoftRegs = 184, kMmaRegs = 48;
+constexpr int kCols = 32;                    // rows of the group a softmax thread holds
+constexpr int kSoftWarps = 12;
+
+// Warps: fill, softmax (12), MMA (2 of 4).  A bf16 cache is filled by TMA from one thread a ring;
+// 4-bit rows are converted by four warps a ring.  Registers a thread at launch, then of each kind
+// of warp; the shares of the warpgroups add up to the launch's: 96 + 3 * 112 + 48 = 5 * 96 and
+// 2 * 64 + 3 * 104 + 40 = 6 * 80.
+template <bool FP4>
+struct Roles {
+  static constexpr int kFill = FP4 ? 8 : 4, kMma = kFill + kSoftWarps, kThreads = (kMma + 4) * 32;
+  static constexpr int kFillRegs = FP4 ? 64 : 96, kSoftRegs = FP4 ? 104 : 112, kMmaRegs = FP4 ? 40 : 48;
+};
 constexpr uint32_t kTmemS = 4 * kRows;       // O^T block j at 96 j, the scores behind them
 constexpr uint64_t kDrainNs = 200ull * 1000 * 1000;
 constexpr float kUnset = -1e38f;             // reference of a row without a token so far
@@ -72,6 +81,11 @@ struct Plan {          // header of the workspace
   int32_t groups;
   int32_t bad;         // malformed offsets
   int32_t spoiled;     // entries of Ws::spoiled
+  int32_t merges;      // entries of Ws::merge
+};
+
+struct Merge {         // a group whose tiles lie in the shares of several blocks
+  int32_t row0, nrows, first, last;   // its rows; the first and the last of the blocks
 };
 
 struct Ws {
@@ -80,6 +94,7 @@ struct Ws {
   Group* group;         // [max groups]
   int64_t* tile0;       // [max groups + 1] first tile of each group
   int32_t* spoiled;     // [T * H] rows of out to compute again
+  Merge* merge;         // [blocks]
   float2* ml;           // [2 * blocks][96] reference and sum of the piece's rows
   float* o;             // [2 * blocks][96][512]
   int64_t max_groups;
@@ -106,6 +121,7 @@ Ws carve(void* base, int64_t T, int64_t B, int64_t H, int blocks) {
   w.group = reinterpret_cast<Group*>(take(sizeof(Group) * w.max_groups));
   w.tile0 = reinterpret_cast<int64_t*>(take(8 * (w.max_groups + 1)));
   w.spoiled = reinterpret_cast<int32_t*>(take(4 * T * H));
+  w.merge = reinterpret_cast<Merge*>(take(sizeof(Merge) * blocks));
   w.ml = reinterpret_cast<float2*>(take(sizeof(float2) * kRows * 2 * blocks));
   w.o = reinterpret_cast<float*>(take(4 * kSlotFloats * 2 * blocks));
   w.bytes = off;
@@ -157,7 +173,18 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* warp_sums) {
   return v + (warp ? warp_sums[warp - 1] : 0);
 }
 
-__global__ void __launch_bounds__(kPlanThreads) latent_plan_kernel(Params p) {
+// The tiles [a, b) of a block's share, and the block whose share holds tile x.
+__device__ __forceinline__ void share(int64_t tiles, int block, int blocks, int64_t* a, int64_t* b) {
+  *a = tiles * block / blocks;
+  *b = tiles * (block + 1) / blocks;
+}
+__device__ __forceinline__ int share_of(int64_t tiles, int64_t x, int blocks) {
+  return static_cast<int>(((x + 1) * blocks - 1) / tiles);
+}
+
+__global__ void __launch_bounds__(kPlanThreads) latent_plan_kernel(Params p, int blocks) {
+  asm volatile("griddepcontrol.launch_dependents;");
+
   __shared__ int64_t sums[32];
   const Ws& w = p.ws;
   const int tid = threadIdx.x;
@@ -174,6 +201,7 @@ __global__ void __launch_bounds__(kPlanThreads) latent_plan_kernel(Params p) {
       w.plan->groups = 0;
       w.plan->bad = 1;
       w.plan->spoiled = 0;
+      w.plan->merges = 0;
       atomicOr(p.err, kErrOffsets);
     }
     return;
@@ -244,22 +272,68 @@ __global__ void __launch_bounds__(kPlanThreads) latent_plan_kernel(Params p) {
     w.plan->bad = 0;
     w.plan->spoiled = 0;
   }
-}
-
-// The tiles [a, b) of a block's share.
-__device__ __forceinline__ void share(int64_t tiles, int block, int blocks, int64_t* a, int64_t* b) {
-  *a = tiles * block / blocks;
-  *b = tiles * (block + 1) / blocks;
+  // groups that several blocks share
+  int* const count = reinterpret_cast<int*>(sums);
+  __syncthreads();
+  if (tid == 0) *count = 0;
+  __syncthreads();
+  for (int g = tid; g < groups; g += kPlanThreads) {
+    const int first = share_of(tiles, w.tile0[g], blocks), last = share_of(tiles, w.tile0[g + 1] - 1, blocks);
+    if (first != last) w.merge[atomicAdd(count, 1)] = Merge{w.group[g].row0, w.group[g].nrows, first, last};
+  }
+  __syncthreads();
+  if (tid == 0) w.plan->merges = *count;
 }
 
 // ---------------------------------------------------------------- pieces of PTX
-__device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t lbo, uint32_t sbo) {
-  // MN-major operand, 128-byte swizzle: 64 values along M/N per 128-byte row, `lbo` bytes to the
-  // next 64, `sbo` to the next 8 rows along K
-  return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>((lbo >> 4) & 0x3FFFu) << 16) |
-         (static_cast<uint64_t>((sbo >> 4) & 0x3FFFu) << 32) | (static_cast<uint64_t>(1) << 46) |
-         (static_cast<uint64_t>(2) << 61);
+// Shared-memory operand descriptors, 128-byte swizzle, 1,024 bytes from 8 rows to the next 8.  The
+// low word holds the address and the leading offset: for a K-major operand (rows along M/N, 64
+// values of K per 128-byte row) the latter is not used; for an MN-major one (rows along K, 64
+// values along M/N) it is the distance to the next 64 values.  Addresses stay below 2^18, so the
+// low word is advanced by plain additions of bytes / 16.
+__device__ __forceinline__ uint32_t desc_lo(uint32_t addr, uint32_t lead) {
+  return ((addr >> 4) & 0x3FFFu) | ((lead >> 4) << 16);
 }
+constexpr uint32_t kDescHi = (1024u >> 4) | (1u << 14) | (2u << 29);
+
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t.reg .b32 x;\n\t"
+      "elect.sync x|p, 0xffffffff;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r));
+  return r != 0;
+}
+
+// D (+)= A . B by the elected lane
+__device__ __forceinline__ void umma_lo(uint32_t d, uint32_t a_lo, uint32_t b_lo, uint32_t idesc, bool accumulate,
+                                        bool leader) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+      "mov.b64 a, {%1, %3};\n\tmov.b64 b, {%2, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %4, p;\n\t}" ::"r"(d),
+      "r"(a_lo), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"((uint32_t)accumulate), "r"((uint32_t)leader)
+      : "memory");
+}
+
+// fetch of `bytes` (a multiple of 16) from a 16-byte aligned address into L2
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
+// position in a ring of N stages and the parity of its full barriers
+template <int N>
+struct Ring {
+  uint32_t s = 0, phase = 0;
+  __device__ __forceinline__ void next() {
+    if (++s == N) {
+      s = 0;
+      phase ^= 1;
+    }
+  }
+};
 
 __device__ __forceinline__ float ex2_approx(float x) {   // relative error near 2^-22; 2^-inf = 0
   float y;
@@ -273,29 +347,52 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return d;
 }
 
-__device__ __forceinline__ float warp_max(float v) {
+// Lane c gets the maximum (or the sum) over the warp of v[c]: each step exchanges half of what is
+// left, 31 shuffles in all (one reduction a column took 160, and the path runs cold).
+template <bool MAX>
+__device__ __forceinline__ float reduce_columns(float (&v)[kCols], int lane) {
 #pragma unroll
-  for (int d = 16; d; d >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, d));
-  return v;
+  for (int w = 16; w; w >>= 1) {
+    const bool up = lane & w;
+#pragma unroll
+    for (int i = 0; i < w; ++i) {
+      const float got = __shfl_xor_sync(0xffffffffu, up ? v[i] : v[i + w], w);
+      const float own = up ? v[i + w] : v[i];
+      v[i] = MAX ? fmaxf(own, got) : own + got;
+    }
+  }
+  return v[0];
 }
 
-// 48 consecutive fp32 columns of the warp's TMEM lanes, and the wait for them
-__device__ __forceinline__ void tmem_ld48(uint32_t a, float (&x)[48]) {
-  uint32_t r[48];
+// 16 consecutive fp32 columns of the warp's TMEM lanes, and the wait for them
+__device__ __forceinline__ void tmem_ld16(uint32_t a, float (&x)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7]), "=f"(x[8]),
+        "=f"(x[9]), "=f"(x[10]), "=f"(x[11]), "=f"(x[12]), "=f"(x[13]), "=f"(x[14]), "=f"(x[15])
+      : "r"(a)
+      : "memory");
+}
+
+__device__ __forceinline__ void tmem_st16(uint32_t a, const float (&x)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};\n\t"
+      "tcgen05.wait::st.sync.aligned;" ::"r"(a),
+      "f"(x[0]), "f"(x[1]), "f"(x[2]), "f"(x[3]), "f"(x[4]), "f"(x[5]), "f"(x[6]), "f"(x[7]), "f"(x[8]), "f"(x[9]),
+      "f"(x[10]), "f"(x[11]), "f"(x[12]), "f"(x[13]), "f"(x[14]), "f"(x[15])
+      : "memory");
+}
+
+// 32 consecutive fp32 columns of the warp's TMEM lanes, and the wait for them
+__device__ __forceinline__ void tmem_ld32(uint32_t a, float (&x)[kCols]) {
+  uint32_t r[32];
+  tmem_ld_32cols(a, r);
+  tmem_ld_wait(r);
 #pragma unroll
-  for (int i = 0; i < 3; ++i)
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(r[16 * i]), "=r"(r[16 * i + 1]), "=r"(r[16 * i + 2]), "=r"(r[16 * i + 3]), "=r"(r[16 * i + 4]),
-          "=r"(r[16 * i + 5]), "=r"(r[16 * i + 6]), "=r"(r[16 * i + 7]), "=r"(r[16 * i + 8]), "=r"(r[16 * i + 9]),
-          "=r"(r[16 * i + 10]), "=r"(r[16 * i + 11]), "=r"(r[16 * i + 12]), "=r"(r[16 * i + 13]),
-          "=r"(r[16 * i + 14]), "=r"(r[16 * i + 15])
-        : "r"(a + 16 * i)
-        : "memory");
-  asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-  for (int i = 0; i < 48; ++i) asm volatile("mov.b32 %0, %1;" : "=f"(x[i]) : "r"(r[i]));
+  for (int i = 0; i < 32; ++i) x[i] = __uint_as_float(r[i]);
 }
 
 // ---------------------------------------------------------------- 4-bit rows
@@ -361,21 +458,23 @@ __device__ __forceinline__ void fp4_store(uint8_t* dst_row, int r, const Fp4Chun
 
 // ---------------------------------------------------------------- attention
 struct alignas(16) Misc {
-  uint64_t full[kStages], empty[kStages], zero_req[kStages], zeroed[kStages];
+  uint64_t full_s[kSStages], empty_s[kSStages];
+  uint64_t full_v[kVStages], empty_v[kVStages], zero_req[kVStages], zeroed[kVStages];
   uint64_t q_full, q_empty, s_full, s_empty, p_full, pv_done, mma_done;
   uint32_t tmem;
   int abort;
   int first_group;
   int pad;
-  alignas(16) float m[kRows];        // reference of each row (log2 units)
+  alignas(16) float nm[kRows];       // minus the reference of each row (log2 units)
   alignas(16) float f[kRows];        // factor of a raised reference; at the end 1 / sum
   alignas(16) int limit[kRows];      // last position the row attends to
-  alignas(16) float red[kSoftWarps][48];
+  alignas(16) float red[kSoftWarps][kCols];
   int spoiled[kRows];                // the row's sums hold a NaN that its weights do not
 };
 
 constexpr int kOffRing = kQBytes;
-constexpr int kOffP = kOffRing + kStages * kStage;
+constexpr int kOffRingV = kOffRing + kSStages * kStage;
+constexpr int kOffP = kOffRingV + kVStages * kStage;
 constexpr int kOffMisc = kOffP + 2 * kPHalf;
 constexpr int kSmem = kOffMisc + static_cast<int>(sizeof(Misc)) + 1024;
 static_assert(kSmem <= 232448, "shared memory per block");
@@ -416,21 +515,28 @@ __device__ __forceinline__ int tile_tokens(const Group& g, int t) {
 }
 
 template <bool FP4>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
     latent_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmC, Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* const sQ = smem;
   uint8_t* const sRing = smem + kOffRing;
+  uint8_t* const sRingV = smem + kOffRingV;
   uint8_t* const sP = smem + kOffP;
   Misc& mi = *reinterpret_cast<Misc*>(smem + kOffMisc);
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  using R = Roles<FP4>;
+  constexpr int kMmaWarp = R::kMma;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const Ws& w = p.ws;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kStages; ++s) {
-      mbar_init(&mi.full[s], FP4 ? kFillWarps * 32 : 1);
-      mbar_init(&mi.empty[s], 1);
+    for (int s = 0; s < kSStages; ++s) {
+      mbar_init(&mi.full_s[s], FP4 ? 128 : 1);
+      mbar_init(&mi.empty_s[s], 1);
+    }
+    for (int s = 0; s < kVStages; ++s) {
+      mbar_init(&mi.full_v[s], FP4 ? 128 : 1);
+      mbar_init(&mi.empty_v[s], 1);
       mbar_init(&mi.zero_req[s], 1);
       mbar_init(&mi.zeroed[s], 1);
     }
@@ -440,7 +546,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(&mi.s_empty, kSoftWarps);
     mbar_init(&mi.p_full, kSoftWarps);
     mbar_init(&mi.pv_done, 1);
-    mbar_init(&mi.mma_done, 1);
+    mbar_init(&mi.mma_done, 2);
     mi.abort = 0;
     fence_mbar_init();
   }
@@ -448,6 +554,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(&mi.tmem, 512);
     tmem_relinquish();
   }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   int64_t a0, a1;
   share(w.plan->tiles, blockIdx.x, gridDim.x, &a0, &a1);
   if (warp == 0 && a0 < a1) {
@@ -465,74 +572,55 @@ __global__ void __launch_bounds__(kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = mi.tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, mi.tmem, 0);
   const WaitCtl wc{p.err, &mi.abort, p.timeout_ns};
   Walk walk(w, a0, a1, mi.first_group);
   Piece pc;
 
-  if (warp < kFillWarps) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kFillRegs));
+  if (warp < R::kFill) {
+    if (FP4) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kFillRegs));
     // ============================================================ fill
-    uint32_t it = 0;        // ring stages so far
-    uint32_t segs = 0;
-    bool ok = true;
-    if (!FP4 && warp == 2) {
-      // zero the rows of a group's last tile that its MMAs read behind its last token
-      uint32_t ph = 0;      // per-stage phase bits of zero_req
-      while (ok && walk.next(&pc)) {
-        if (pc.g.ntok == 0) continue;
-        uint32_t stages = 0;
-        for (int t = 0; t < pc.n; ++t) stages += 9 + (tile_tokens(pc.g, pc.t0 + t) > 64 ? 8 : 4);
-        const int v = tile_tokens(pc.g, pc.t0 + pc.n - 1);
-        if (pc.last && (v & 15)) {
-          const int halves = v > 64 ? 2 : 1;
-          const int r0 = v - 64 * (halves - 1), r1 = (r0 + 15) & ~15;
-          for (int j = 0; j < 4 && ok; ++j) {
-            const uint32_t at = it + stages - 4 * halves + j * halves + (halves - 1), s = at % kStages;
-            ok = mbar_wait(&mi.zero_req[s], (ph >> s) & 1, wc) && mbar_wait(&mi.full[s], (at / kStages) & 1, wc);
-            if (!ok) break;
-            ph ^= 1u << s;
-            for (int u = lane; u < (r1 - r0) * 16; u += 32) {
-              const int r = r0 + (u >> 4), un = u & 15;
-              *reinterpret_cast<uint4*>(sRing + s * kStage + (un >> 3) * 8192 + r * 128 + (un & 7) * 16) =
-                  make_uint4(0u, 0u, 0u, 0u);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&mi.zeroed[s]);
-          }
-        }
-        it += stages;
+    // stage `it` of a ring may be written once its previous contents have been read
+    auto acquire = [&](uint64_t* empty, uint32_t it, uint32_t n) {
+      return it < n || mbar_wait(&empty[it % n], (it / n - 1) & 1, wc);
+    };
+    // on an early exit the loads in flight land before the block ends
+    auto drain = [&](uint64_t* bar, uint32_t parity) {
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try_wait(smem_u32(bar), parity) && global_timer_ns() - t0 <= kDrainNs) {
       }
-    } else if (FP4 || (warp == 0 && lane == 0)) {
-      const int i = threadIdx.x;       // FP4: token of the tile (scores), token and half (values)
-      auto q_load = [&]() {
-        if (segs > 0 && !mbar_wait(&mi.q_empty, (segs - 1) & 1, wc)) return false;
-        mbar_arrive_expect_tx(&mi.q_full, kQBytes);
-        for (int c = 0; c < 9; ++c) tma_load_2d(sQ + c * kQChunk, &tmQ, &mi.q_full, 64 * c, pc.g.row0);
-        return true;
-      };
-      auto acquire = [&](uint32_t s) { return it < kStages || mbar_wait(&mi.empty[s], (it / kStages - 1) & 1, wc); };
+    };
+    uint32_t it = 0;        // stages of the warp's ring so far
+    uint32_t segs = 0;      // pieces so far
+    bool ok = true;
+    auto q_load = [&]() {
+      if (segs > 0 && !mbar_wait(&mi.q_empty, (segs - 1) & 1, wc)) return false;
+      mbar_arrive_expect_tx(&mi.q_full, kQBytes);
+      for (int c = 0; c < 9; ++c) tma_load_2d(sQ + c * kQChunk, &tmQ, &mi.q_full, 64 * c, pc.g.row0);
+      return true;
+    };
+    if constexpr (FP4) {
+      const int i = threadIdx.x & 127;     // token of the tile (scores), token and half (values)
+      const bool scores = warp < 4;
       while (ok && walk.next(&pc)) {
         if (pc.g.ntok == 0) continue;
-        if (!FP4 || i == 0) ok = q_load();
-        ++segs;
-        if constexpr (FP4) {
-          const uint8_t* const base = p.kv4 + pc.g.kv_row0 * kLatRow4;
-          const int32_t* const sel =
-              p.k_sel >= 0 ? p.idx + static_cast<int64_t>(pc.g.row0 / p.H) * p.k_sel : nullptr;
-          // cache row of token j of tile t, or null
-          auto row_of = [&](int t, int j) -> const uint8_t* {
-            const int k = t * kTile + j;
-            if (k >= pc.g.ntok) return nullptr;
-            int pos = k;
-            if (sel) {
-              pos = sel[k];
-              if (pos >= pc.g.seq_len) atomicOr(p.err, kErrBounds);
-              if (pos < 0 || pos >= pc.g.seq_len) return nullptr;
-            }
-            return base + static_cast<int64_t>(pos) * kLatRow4;
-          };
+        const uint8_t* const base = p.kv4 + pc.g.kv_row0 * kLatRow4;
+        const int32_t* const sel = p.k_sel >= 0 ? p.idx + static_cast<int64_t>(pc.g.row0 / p.H) * p.k_sel : nullptr;
+        // cache row of token j of tile t, or null
+        auto row_of = [&](int t, int j) -> const uint8_t* {
+          const int k = t * kTile + j;
+          if (k >= pc.g.ntok) return nullptr;
+          int pos = k;
+          if (sel) {
+            pos = sel[k];
+            if (pos >= pc.g.seq_len) atomicOr(p.err, kErrBounds);
+            if (pos < 0 || pos >= pc.g.seq_len) return nullptr;
+          }
+          return base + static_cast<int64_t>(pos) * kLatRow4;
+        };
+        if (scores) {
+          if (i == 0) ok = q_load();
+          ++segs;
           auto prefetch = [&](int t) {
             if (t >= pc.t0 + pc.n) return;
             const uint8_t* r = row_of(t, i);
@@ -540,36 +628,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int k = 0; k < 4; ++k) asm volatile("prefetch.global.L2 [%0];" ::"l"(r + 128 * k));
             asm volatile("prefetch.global.L2 [%0];" ::"l"(r + kLatRow4 - 16));
-          };
-          auto values = [&](int t) {
-            const int v = tile_tokens(pc.g, t);
-            const int halves = v > 64 ? 2 : 1;
-            const int j = i & 63, sub = i >> 6;
-            const uint8_t* r[2] = {row_of(t, j), halves == 2 ? row_of(t, 64 + j) : nullptr};
-            Fp4Chunk nx = {};
-            if (r[0]) nx = fp4_load(r[0], sub);
-            for (int k = 0; k < 4 * halves; ++k) {
-              const int hf = halves == 2 ? k & 1 : 0;
-              const Fp4Chunk cur = nx;
-              const bool have = r[hf] != nullptr;
-              if (k + 1 < 4 * halves) {
-                const int hn = halves == 2 ? (k + 1) & 1 : 0, blk = halves == 2 ? (k + 1) >> 1 : k + 1;
-                if (r[hn]) nx = fp4_load(r[hn], 2 * blk + sub);
-              }
-              const uint32_t s = it % kStages;
-              if (!acquire(s)) return false;
-              uint8_t* const dst = sRing + s * kStage + sub * 8192 + j * 128;
-              if (have) {
-                fp4_store(dst, j, cur);
-              } else {
-#pragma unroll
-                for (int u = 0; u < 8; ++u) reinterpret_cast<uint4*>(dst)[u] = make_uint4(0u, 0u, 0u, 0u);
-              }
-              fence_proxy_async_smem();
-              mbar_arrive(&mi.full[s]);
-              ++it;
-            }
-            return true;
           };
           prefetch(pc.t0);
           for (int t = pc.t0; t < pc.t0 + pc.n && ok; ++t) {
@@ -580,8 +638,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int c = 0; c < 9; ++c) {
               const Fp4Chunk cur = nx;
               if (r && c + 1 < 8) nx = fp4_load(r, c + 1);
-              const uint32_t s = it % kStages;
-              if (!(ok = acquire(s))) break;
+              if (!(ok = acquire(mi.empty_s, it, kSStages))) break;
+              const uint32_t s = it % kSStages;
               uint8_t* const dst = sRing + s * kStage + i * 128;
               if (r && c < 8) {
                 fp4_store(dst, i, cur);
@@ -592,124 +650,194 @@ __global__ void __launch_bounds__(kThreads, 1)
                       reinterpret_cast<const uint4*>(r + kLatCodes + kLatScales)[u];
               }   // a missing token's score is masked, whatever its row holds
               fence_proxy_async_smem();
-              mbar_arrive(&mi.full[s]);
+              mbar_arrive(&mi.full_s[s]);
               ++it;
             }
-            if (ok && t > pc.t0) ok = values(t - 1);
           }
-          if (ok) ok = values(pc.t0 + pc.n - 1);
         } else {
-          auto load = [&](int x0, int x1, int y0, int y1, bool two, bool zero) {
-            const uint32_t s = it % kStages;
-            if (!acquire(s)) return false;
-            mbar_arrive_expect_tx(&mi.full[s], two ? kStage : kStage / 2);
-            tma_load_2d(sRing + s * kStage, &tmC, &mi.full[s], x0, y0);
-            if (two) tma_load_2d(sRing + s * kStage + kStage / 2, &tmC, &mi.full[s], x1, y1);
-            if (zero) mbar_arrive(&mi.zero_req[s]);
-            ++it;
-            return true;
-          };
-          const int y = static_cast<int>(pc.g.kv_row0);
-          auto values = [&](int t) {
-            const int v = tile_tokens(pc.g, t), halves = v > 64 ? 2 : 1;
-            for (int j = 0; j < 4; ++j)
-              for (int hf = 0; hf < halves; ++hf) {
-                const int yy = y + t * kTile + 64 * hf;
-                if (!load(128 * j, 128 * j + 64, yy, yy, true, hf == halves - 1 && (v & 15))) return false;
-              }
-            return true;
-          };
           for (int t = pc.t0; t < pc.t0 + pc.n && ok; ++t) {
-            const bool two = tile_tokens(pc.g, t) > 64;
-            const int yy = y + t * kTile;
-            for (int c = 0; c < 9 && ok; ++c) ok = load(64 * c, 64 * c, yy, yy + 64, two, false);
-            if (ok && t > pc.t0) ok = values(t - 1);
+            const int halves = tile_tokens(pc.g, t) > 64 ? 2 : 1;
+            const int j = i & 63, part = i >> 6;
+            const uint8_t* const r0 = row_of(t, j);
+            const uint8_t* const r1 = halves == 2 ? row_of(t, 64 + j) : nullptr;
+            Fp4Chunk nx = {};
+            if (r0) nx = fp4_load(r0, part);
+            for (int k = 0; k < 4 * halves; ++k) {
+              const Fp4Chunk cur = nx;
+              const bool have = (halves == 2 && (k & 1) ? r1 : r0) != nullptr;
+              if (k + 1 < 4 * halves) {
+                const uint8_t* const rn = halves == 2 && !(k & 1) ? r1 : r0;
+                if (rn) nx = fp4_load(rn, 2 * (halves == 2 ? (k + 1) >> 1 : k + 1) + part);
+              }
+              if (!(ok = acquire(mi.empty_v, it, kVStages))) break;
+              const uint32_t s = it % kVStages;
+              uint8_t* const dst = sRingV + s * kStage + part * 8192 + j * 128;
+              if (have) {
+                fp4_store(dst, j, cur);
+              } else {
+#pragma unroll
+                for (int u = 0; u < 8; ++u) reinterpret_cast<uint4*>(dst)[u] = make_uint4(0u, 0u, 0u, 0u);
+              }
+              fence_proxy_async_smem();
+              mbar_arrive(&mi.full_v[s]);
+              ++it;
+            }
           }
-          if (ok) ok = values(pc.t0 + pc.n - 1);
         }
       }
-      if (!FP4 || i == 0) {
-        // on an early exit the loads in flight land before the block ends
-        if (!ok) {
-          auto drain = [&](uint64_t* bar, uint32_t parity) {
-            const uint64_t t0 = global_timer_ns();
-            while (!mbar_try_wait(smem_u32(bar), parity) && global_timer_ns() - t0 <= kDrainNs) {
-            }
-          };
-          if (!FP4)
-            for (uint32_t k = it > kStages ? it - kStages : 0; k < it; ++k) drain(&mi.full[k % kStages], (k / kStages) & 1);
-          if (segs > 0) drain(&mi.q_full, (segs - 1) & 1);
+      if (scores && i == 0 && !ok && segs > 0) drain(&mi.q_full, (segs - 1) & 1);
+    } else if (warp == 0 && lane == 0) {
+      // scores: nine 64-value chunks of a tile; the next tile is fetched into L2 meanwhile, since
+      // the ring alone holds less than the memory's latency asks for
+      while (ok && walk.next(&pc)) {
+        if (pc.g.ntok == 0) continue;
+        ok = q_load();
+        ++segs;
+        for (int t = pc.t0; t < pc.t0 + pc.n && ok; ++t) {
+          const bool two = tile_tokens(pc.g, t) > 64;
+          const int y = static_cast<int>(pc.g.kv_row0) + t * kTile;
+          // bytes of the next tile, fetched in order (rows follow one another, while a stage's loads
+          // touch 128 bytes of each)
+          const int ahead = t + 1 < pc.t0 + pc.n ? tile_tokens(pc.g, t + 1) * 2 * kLatDim : 0;
+          const uint8_t* const src = reinterpret_cast<const uint8_t*>(p.kv + static_cast<int64_t>(y + kTile) * kLatDim);
+          for (int c = 0; c < 9; ++c) {
+            if (!(ok = acquire(mi.empty_s, it, kSStages))) break;
+            const uint32_t s = it % kSStages;
+            mbar_arrive_expect_tx(&mi.full_s[s], two ? kStage : kStage / 2);
+            tma_load_2d(sRing + s * kStage, &tmC, &mi.full_s[s], 64 * c, y);
+            if (two) tma_load_2d(sRing + s * kStage + kStage / 2, &tmC, &mi.full_s[s], 64 * c, y + 64);
+            if (ahead > c * kStage) prefetch_l2(src + c * kStage, ahead - c * kStage < kStage ? ahead - c * kStage : kStage);
+            ++it;
+          }
         }
+      }
+      if (!ok) {
+        for (uint32_t k = it > kSStages ? it - kSStages : 0; k < it; ++k)
+          drain(&mi.full_s[k % kSStages], (k / kSStages) & 1);
+        if (segs > 0) drain(&mi.q_full, (segs - 1) & 1);
+      }
+    } else if (warp == 1 && lane == 0) {
+      // values: 64 tokens x 128 dims a stage
+      while (ok && walk.next(&pc)) {
+        if (pc.g.ntok == 0) continue;
+        for (int t = pc.t0; t < pc.t0 + pc.n && ok; ++t) {
+          const int v = tile_tokens(pc.g, t), halves = v > 64 ? 2 : 1;
+          for (int k = 0; k < 4 * halves; ++k) {
+            const int j = halves == 2 ? k >> 1 : k, hf = halves == 2 ? k & 1 : 0;
+            const int y = static_cast<int>(pc.g.kv_row0) + t * kTile + 64 * hf;
+            if (!(ok = acquire(mi.empty_v, it, kVStages))) break;
+            const uint32_t s = it % kVStages;
+            mbar_arrive_expect_tx(&mi.full_v[s], kStage);
+            tma_load_2d(sRingV + s * kStage, &tmC, &mi.full_v[s], 128 * j, y);
+            tma_load_2d(sRingV + s * kStage + kStage / 2, &tmC, &mi.full_v[s], 128 * j + 64, y);
+            if (hf == halves - 1 && (v & 15)) mbar_arrive(&mi.zero_req[s]);
+            ++it;
+          }
+        }
+      }
+      if (!ok)
+        for (uint32_t k = it > kVStages ? it - kVStages : 0; k < it; ++k)
+          drain(&mi.full_v[k % kVStages], (k / kVStages) & 1);
+    } else if (warp == 2) {
+      // zero the rows of a group's last tile that its MMAs read behind its last token
+      uint32_t ph = 0;      // per-stage phase bits of zero_req
+      while (ok && walk.next(&pc)) {
+        if (pc.g.ntok == 0) continue;
+        uint32_t stages = 0;
+        for (int t = 0; t < pc.n; ++t) stages += tile_tokens(pc.g, pc.t0 + t) > 64 ? 8 : 4;
+        const int v = tile_tokens(pc.g, pc.t0 + pc.n - 1);
+        if (pc.last && (v & 15)) {
+          const int halves = v > 64 ? 2 : 1;
+          const int r0 = v - 64 * (halves - 1), r1 = (r0 + 15) & ~15;
+          for (int j = 0; j < 4 && ok; ++j) {
+            const uint32_t at = it + stages - 4 * halves + j * halves + (halves - 1), s = at % kVStages;
+            ok = mbar_wait(&mi.zero_req[s], (ph >> s) & 1, wc) && mbar_wait(&mi.full_v[s], (at / kVStages) & 1, wc);
+            if (!__all_sync(0xffffffffu, ok)) {
+              ok = false;
+              break;
+            }
+            ph ^= 1u << s;
+            for (int u = lane; u < (r1 - r0) * 16; u += 32) {
+              const int r = r0 + (u >> 4), un = u & 15;
+              *reinterpret_cast<uint4*>(sRingV + s * kStage + (un >> 3) * 8192 + r * 128 + (un & 7) * 16) =
+                  make_uint4(0u, 0u, 0u, 0u);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&mi.zeroed[s]);
+          }
+        }
+        it += stages;
       }
     }
+    __syncwarp();
   } else if (warp < kMmaWarp) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(R::kSoftRegs));
     // ============================================================ softmax
-    const int wg = (warp - kFillWarps) >> 2, qd = warp & 3;
+    const int wg = (warp - R::kFill) >> 2, qd = warp & 3;
     const int tok = qd * 32 + lane;                       // token of the tile, TMEM lane
     const uint32_t tlane = tmem + (static_cast<uint32_t>(qd * 32) << 16);
-    const int wtid = (warp - kFillWarps - 4 * wg) * 32 + lane;
+    const int wtid = (warp - R::kFill - 4 * wg) * 32 + lane;
     const int bar_id = 1 + wg;
     uint32_t done = 0;      // tiles so far
     // A wait that ran out is skipped from then on, but the walk goes on to its end: the warps of
-    // a half meet at named barriers and none may leave the others there.  The results are then
+    // a third meet at named barriers and none may leave the others there.  The results are then
     // worthless, and the error word says so.
     bool ok = true;
     while (walk.next(&pc)) {
       const Group& g = pc.g;
-      // columns (rows of the group) of this half: the N of the MMAs split into two runs of 16s
-      const int n16 = (g.nrows + 15) / 16, c0 = wg ? (n16 + 1) / 2 * 16 : 0;
-      const int nc = wg ? n16 * 16 - c0 : (n16 + 1) / 2 * 16;
-      // rows' references and limits
+      // columns (rows of the group) of this third, of the N of the MMAs
+      const int n16 = (g.nrows + 15) / 16 * 16, c0 = kCols * wg;
+      const int nc = n16 - c0 < 0 ? 0 : n16 - c0 < kCols ? n16 - c0 : kCols;
+      // rows' references and limits; columns without a row never raise theirs and weigh nothing
       int lim = -1;
-      if (wtid < nc) {
+      if (wtid < kCols) {
         const int r = c0 + wtid;
+        const bool real = r < g.nrows;
         if (p.k_sel >= 0) {
           lim = 0;
-        } else if (r < g.nrows) {
+        } else if (real) {
           lim = p.positions[(g.row0 + r) / p.H];
           if (lim >= g.seq_len || lim < -1) lim = -1;
         }
-        mi.m[r] = kUnset;
+        mi.nm[r] = real ? -kUnset : -INFINITY;
         mi.limit[r] = lim;
         mi.spoiled[r] = 0;
+        if (!real) lim = 0x7FFFFFFF;
+      } else {
+        lim = 0x7FFFFFFF;
       }
-      // padding rows (r >= nrows) ask for nothing and may be masked or not
-      const int mine = wtid < nc && c0 + wtid < g.nrows ? lim : 0x7FFFFFFF;
-      int low = __reduce_min_sync(0xffffffffu, mine);
-      if (lane == 0) mi.red[warp - kFillWarps][0] = __int_as_float(low);
+      int low = __reduce_min_sync(0xffffffffu, lim);   // of the third's rows (all in its first warp)
+      if (wtid == 0) mi.red[warp - R::kFill][0] = __int_as_float(low);
       named_bar_sync(bar_id, 128);
-      for (int k = 0; k < 4; ++k) {
-        const int o = __float_as_int(mi.red[4 * wg + k][0]);
-        low = o < low ? o : low;
-      }
+      low = __float_as_int(mi.red[4 * wg][0]);
       named_bar_sync(bar_id, 128);
-      float l[48];
+      float2 l[kCols / 2];
 #pragma unroll
-      for (int c = 0; c < 48; ++c) l[c] = 0.f;
+      for (int c = 0; c < kCols / 2; ++c) l[c] = make_float2(0.f, 0.f);
       const int32_t* const sel = p.k_sel >= 0 ? p.idx + static_cast<int64_t>(g.row0 / p.H) * p.k_sel : nullptr;
+      const float4* const nm4 = reinterpret_cast<const float4*>(mi.nm + c0);
 
       for (int t = 0; g.ntok > 0 && t < pc.n; ++t, ++done) {
         const int first_pos = (pc.t0 + t) * kTile;
         int pos = first_pos + tok;
-        bool masked = sel || first_pos + kTile - 1 > low;
+        const bool masked = sel || first_pos + kTile - 1 > low;
         if (sel) {
           const int e = pos < g.ntok ? sel[pos] : -1;
           pos = e >= 0 && e < g.seq_len ? 0 : 0x7FFFFFFF;
         }
         ok = ok && __all_sync(0xffffffffu, mbar_wait(&mi.s_full, done & 1, wc));
         tc_fence_after();
-        float x[48];
-        tmem_ld48(tlane + kTmemS + c0, x);
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&mi.s_empty);
-        const float4* const m4 = reinterpret_cast<const float4*>(mi.m + c0);
-        if (masked) {
-          const int4* const l4 = reinterpret_cast<const int4*>(mi.limit + c0);
+        // y = x - m (log2 units) of the token against the rows, and their maximum
+        float2 y[kCols / 2];
+        float top = -INFINITY;
+        auto scores = [&]() {
+          float x[kCols];
+          tmem_ld32(tlane + kTmemS + c0, x);
+          if (masked) {
+            const int4* const l4 = reinterpret_cast<const int4*>(mi.limit + c0);
 #pragma unroll
-          for (int c = 0; c < 12; ++c) {
-            if (4 * c < nc) {
+            for (int c = 0; c < kCols / 4; ++c) {
               const int4 v = l4[c];
               x[4 * c] = pos <= v.x ? x[4 * c] : -INFINITY;
               x[4 * c + 1] = pos <= v.y ? x[4 * c + 1] : -INFINITY;
@@ -717,48 +845,49 @@ __global__ void __launch_bounds__(kThreads, 1)
               x[4 * c + 3] = pos <= v.w ? x[4 * c + 3] : -INFINITY;
             }
           }
-        }
-        float top = -INFINITY;
 #pragma unroll
-        for (int c = 0; c < 12; ++c) {
-          if (4 * c < nc) {
-            const float4 m = m4[c];
-            top = fmaxf(top, fmaf(x[4 * c], p.scale_log2, -m.x));
-            top = fmaxf(top, fmaf(x[4 * c + 1], p.scale_log2, -m.y));
-            top = fmaxf(top, fmaf(x[4 * c + 2], p.scale_log2, -m.z));
-            top = fmaxf(top, fmaf(x[4 * c + 3], p.scale_log2, -m.w));
+          for (int c = 0; c < kCols / 2; ++c) y[c] = make_float2(x[2 * c], x[2 * c + 1]);
+        };
+        const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
+        auto shift = [&]() {
+#pragma unroll
+          for (int c = 0; c < kCols / 4; ++c) {
+            const float4 m = nm4[c];
+            y[2 * c] = ffma2(y[2 * c], scale2, make_float2(m.x, m.y));
+            y[2 * c + 1] = ffma2(y[2 * c + 1], scale2, make_float2(m.z, m.w));
           }
+        };
+        if (nc > 0) {
+          scores();
+          shift();
+#pragma unroll
+          for (int c = 0; c < kCols / 2; ++c) top = fmaxf(top, fmaxf(y[c].x, y[c].y));
         }
         if (named_bar_or(bar_id, 128, top > 8.f)) {
           // some row's reference rises: the tile's maximum of every row, over the tokens
+          scores();
+          {
+            float v[kCols];
 #pragma unroll
-          for (int c = 0; c < 48; ++c) {
-            if (c < nc) {
-              const float v = warp_max(x[c]);
-              if (lane == (c & 31)) mi.red[warp - kFillWarps][c] = v;
-            }
+            for (int c = 0; c < kCols; ++c) v[c] = c & 1 ? y[c / 2].y : y[c / 2].x;
+            mi.red[warp - R::kFill][lane] = reduce_columns<true>(v, lane);
           }
           named_bar_sync(bar_id, 128);
           if (wtid < nc) {
             float v = -INFINITY;
             for (int k = 0; k < 4; ++k) v = fmaxf(v, mi.red[4 * wg + k][wtid]);
             v *= p.scale_log2;
-            const float old = mi.m[c0 + wtid];
+            const float old = -mi.nm[c0 + wtid];
             const float now = v > old + 8.f ? v : old;
-            mi.m[c0 + wtid] = now;
+            mi.nm[c0 + wtid] = -now;
             mi.f[c0 + wtid] = ex2_approx(old - now);
           }
           named_bar_sync(bar_id, 128);
-          const float4* const f4 = reinterpret_cast<const float4*>(mi.f + c0);
+          shift();
 #pragma unroll
-          for (int c = 0; c < 12; ++c) {
-            if (4 * c < nc) {
-              const float4 f = f4[c];
-              l[4 * c] *= f.x;
-              l[4 * c + 1] *= f.y;
-              l[4 * c + 2] *= f.z;
-              l[4 * c + 3] *= f.w;
-            }
+          for (int c = 0; c < kCols / 2; ++c) {
+            l[c].x *= mi.f[c0 + 2 * c];
+            l[c].y *= mi.f[c0 + 2 * c + 1];
           }
           if (t > 0) {
             // the sums so far, once every earlier product has landed in them
@@ -768,74 +897,51 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int j = 0; j < 4; ++j) {
 #pragma unroll 1
               for (int cc = 0; cc < nc; cc += 16) {
-                uint32_t o[16];
+                float o[16];
                 const uint32_t a = tlane + j * kRows + c0 + cc;
-                asm volatile(
-                    "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-                    "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
-                    "tcgen05.wait::ld.sync.aligned;"
-                    : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7]),
-                      "=r"(o[8]), "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]), "=r"(o[14]),
-                      "=r"(o[15])
-                    : "r"(a)
-                    : "memory");
+                tmem_ld16(a, o);
 #pragma unroll
-                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * mi.f[c0 + cc + k]);
-                asm volatile(
-                    "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
-                    "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};\n\t"
-                    "tcgen05.wait::st.sync.aligned;"
-                    ::"r"(a), "r"(o[0]), "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7]),
-                      "r"(o[8]), "r"(o[9]), "r"(o[10]), "r"(o[11]), "r"(o[12]), "r"(o[13]), "r"(o[14]), "r"(o[15])
-                    : "memory");
+                for (int k = 0; k < 16; ++k) o[k] *= mi.f[c0 + cc + k];
+                tmem_st16(a, o);
               }
             }
           }
         }
-        // weights: 2^(x - m), summed before their rounding to bf16 (lse keeps fp32's precision;
-        // out gets one rounding of up to 2^-8 a weight, the operand type of the product)
-        uint32_t pk[24];
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&mi.s_empty);
+        // weights: 2^y, summed before their rounding to bf16 (lse keeps fp32's precision; out
+        // gets one rounding of up to 2^-8 a weight, the operand type of the product)
+        uint32_t pk[kCols / 2];
+        if (nc > 0) {
 #pragma unroll
-        for (int c = 0; c < 12; ++c) {
-          if (4 * c < nc) {
-            const float4 m = m4[c];
-            const float e0 = ex2_approx(fmaf(x[4 * c], p.scale_log2, -m.x));
-            const float e1 = ex2_approx(fmaf(x[4 * c + 1], p.scale_log2, -m.y));
-            const float e2 = ex2_approx(fmaf(x[4 * c + 2], p.scale_log2, -m.z));
-            const float e3 = ex2_approx(fmaf(x[4 * c + 3], p.scale_log2, -m.w));
-            l[4 * c] += e0;
-            l[4 * c + 1] += e1;
-            l[4 * c + 2] += e2;
-            l[4 * c + 3] += e3;
-            pk[2 * c] = pack2(e0, e1);
-            pk[2 * c + 1] = pack2(e2, e3);
+          for (int c = 0; c < kCols / 2; ++c) {
+            const float2 e = make_float2(ex2_approx(y[c].x), ex2_approx(y[c].y));
+            l[c] = __fadd2_rn(l[c], e);
+            pk[c] = pack2(e.x, e.y);
           }
         }
         // the weights' place in shared memory is free once the previous tile's product is done
         if (done > 0) ok = ok && __all_sync(0xffffffffu, mbar_wait(&mi.pv_done, (done - 1) & 1, wc));
+        if (nc > 0) {
 #pragma unroll
-        for (int u = 0; u < 6; ++u) {
-          if (8 * u < nc) {
+          for (int u = 0; u < kCols / 8; ++u) {
             const int col = c0 + 8 * u;
             *reinterpret_cast<uint4*>(sP + (col >> 6) * kPHalf + tok * 128 + ((((col & 63) >> 3) ^ (tok & 7)) * 16)) =
                 make_uint4(pk[4 * u], pk[4 * u + 1], pk[4 * u + 2], pk[4 * u + 3]);
           }
+          fence_proxy_async_smem();
         }
-        fence_proxy_async_smem();
-        tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&mi.p_full);
       }
       // the rows' sums over the 128 threads
       named_bar_sync(bar_id, 128);
+      {
+        float v[kCols];
 #pragma unroll
-      for (int c = 0; c < 48; ++c) {
-        if (c < nc) {
-          float v = l[c];
-#pragma unroll
-          for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
-          if (lane == (c & 31)) mi.red[warp - kFillWarps][c] = v;
-        }
+        for (int c = 0; c < kCols; ++c) v[c] = c & 1 ? l[c / 2].y : l[c / 2].x;
+        mi.red[warp - R::kFill][lane] = reduce_columns<false>(v, lane);
       }
       named_bar_sync(bar_id, 128);
       const bool whole = pc.first && pc.last;
@@ -846,7 +952,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int r = c0 + wtid;
         mi.f[r] = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
         if (r < g.nrows) {
-          const float m = mi.m[r];
+          const float m = -mi.nm[r];
           if (whole) p.lse[g.row0 + r] = sum == 0.f ? -INFINITY : fmaf(m, 0.69314718055994531f, logf(sum));
           else w.ml[static_cast<int64_t>(slot) * kRows + r] = make_float2(m, sum);
         }
@@ -857,33 +963,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_after();
       }
 #pragma unroll 1
-      for (int j = 0; j < 4; ++j) {
-        float o[48];
-        if (g.ntok > 0) tmem_ld48(tlane + j * kRows + c0, o);
+      for (int u = 0; u < 4 * ((nc + 15) / 16); ++u) {
+        const int j = u & 3, cb = c0 + (u >> 2) * 16;         // block of dims, first of 16 rows
+        float o[16];
+        if (g.ntok > 0) tmem_ld16(tlane + j * kRows + cb, o);
         const int dim = 128 * j + tok;
         if (whole) {
-          __nv_bfloat16* const ob = p.out + static_cast<int64_t>(g.row0 + c0) * kLatV + (dim & ~1);
+          // even lanes keep row c, odd lanes row c + 1, each with its pair of dims
+          __nv_bfloat16* ob = p.out + static_cast<int64_t>(g.row0 + cb + (lane & 1)) * kLatV + (dim & ~1);
 #pragma unroll
-          for (int c = 0; c < 48; c += 2) {
-            if (c < nc) {
-              // even lanes keep row c, odd lanes row c + 1, each with its pair of dims
-              const float i0 = mi.f[c0 + c], i1 = mi.f[c0 + c + 1];
-              const float v0 = i0 != 0.f ? o[c] * i0 : 0.f, v1 = i1 != 0.f ? o[c + 1] * i1 : 0.f;
-              if (!FP4) {
-                if (v0 != v0 && i0 == i0) mi.spoiled[c0 + c] = 1;
-                if (v1 != v1 && i1 == i1) mi.spoiled[c0 + c + 1] = 1;
-              }
-              const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? v0 : v1, 1);
-              const uint32_t pr = lane & 1 ? pack2(got, v1) : pack2(v0, got);
-              const int r = c + (lane & 1);
-              if (c0 + r < g.nrows) *reinterpret_cast<uint32_t*>(ob + static_cast<int64_t>(r) * kLatV) = pr;
+          for (int c = 0; c < 16; c += 2) {
+            const float i0 = mi.f[cb + c], i1 = mi.f[cb + c + 1];
+            const float v0 = i0 != 0.f ? o[c] * i0 : 0.f, v1 = i1 != 0.f ? o[c + 1] * i1 : 0.f;
+            if (!FP4) {
+              if (v0 != v0 && i0 == i0) mi.spoiled[cb + c] = 1;
+              if (v1 != v1 && i1 == i1) mi.spoiled[cb + c + 1] = 1;
             }
+            const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? v0 : v1, 1);
+            const uint32_t pr = lane & 1 ? pack2(got, v1) : pack2(v0, got);
+            if (cb + c + (lane & 1) < g.nrows) *reinterpret_cast<uint32_t*>(ob + c * kLatV) = pr;
           }
         } else {
-          float* const ob = w.o + slot * kSlotFloats + static_cast<int64_t>(c0) * kLatV + dim;
+          float* const ob = w.o + slot * kSlotFloats + static_cast<int64_t>(cb) * kLatV + dim;
 #pragma unroll
-          for (int c = 0; c < 48; ++c)
-            if (c < nc && c0 + c < g.nrows) ob[c * kLatV] = o[c];
+          for (int c = 0; c < 16; ++c)
+            if (cb + c < g.nrows) ob[c * kLatV] = o[c];
         }
       }
       tc_fence_before();
@@ -892,71 +996,91 @@ __global__ void __launch_bounds__(kThreads, 1)
         w.spoiled[atomicAdd(&w.plan->spoiled, 1)] = g.row0 + c0 + wtid;
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kMmaRegs));
-    // ============================================================ MMA issuer
-    if (warp == kMmaWarp && lane == 0) {
-    uint32_t it = 0, done = 0, segs = 0, zph = 0;
-    bool ok = true;
-    const uint32_t qa = smem_u32(sQ), ra = smem_u32(sRing), pa = smem_u32(sP);
-    while (ok && walk.next(&pc)) {
-      const Group& g = pc.g;
-      if (g.ntok == 0) continue;
-      const int N = (g.nrows + 15) / 16 * 16;
-      const uint32_t idesc_s = umma_idesc_bf16(128, N);
-      const uint32_t idesc_o = idesc_s | (1u << 15) | (1u << 16);   // both operands MN-major
-      if (!(ok = mbar_wait(&mi.q_full, segs & 1, wc))) break;
-      ++segs;
-      // O^T += C_latent^T . P^T of the tile `u` of the piece
-      auto values = [&](int u) {
-        const int v = tile_tokens(g, pc.t0 + u), halves = v > 64 ? 2 : 1;
-        const bool zero = !FP4 && pc.last && u == pc.n - 1 && (v & 15);
-        if (!mbar_wait(&mi.p_full, (done - (pc.n - u)) & 1, wc)) return false;
-        for (int j = 0; j < 4; ++j) {
-          for (int hf = 0; hf < halves; ++hf) {
-            const uint32_t s = it % kStages;
-            if (zero && hf == halves - 1) {
-              if (!mbar_wait(&mi.zeroed[s], (zph >> s) & 1, wc)) return false;
-              zph ^= 1u << s;
-            }
-            if (!mbar_wait(&mi.full[s], (it / kStages) & 1, wc)) return false;
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(R::kMmaRegs));
+    // ============================================================ MMA issuers
+    // One warp for the scores, one for the values: issuing takes 73 and 117 cycles an instruction
+    // (its operands move to uniform registers), more than the 56 it runs for.  The whole warp walks
+    // along and one elected lane issues (with a single lane in the loop 150 and 240 cycles).
+    if (warp < kMmaWarp + 2) {
+      const bool leader = elect_one();
+      bool ok = true;
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity, wc)); };
+      auto commit = [&](uint64_t* bar) {
+        if (leader) umma_commit(bar);
+      };
+      uint32_t nth = 0;       // tiles so far
+      if (warp == kMmaWarp) {
+        Ring<kSStages> rg;
+        uint32_t segs = 0;
+        const uint32_t q_lo = desc_lo(smem_u32(sQ), 16), r_lo = desc_lo(smem_u32(sRing), 16);   // K-major
+        while (ok && walk.next(&pc)) {
+          if (pc.g.ntok == 0) continue;
+          const uint32_t idesc = umma_idesc_bf16(128, (pc.g.nrows + 15) / 16 * 16);
+          if (!(ok = wait(&mi.q_full, segs & 1))) break;
+          ++segs;
+          for (int t = 0; t < pc.n && ok; ++t, ++nth) {
+            if (nth > 0 && !(ok = wait(&mi.s_empty, (nth - 1) & 1))) break;
             tc_fence_after();
-            const int left = v - 64 * hf, steps = left >= 64 ? 4 : (left + 15) / 16;
-            for (int k = 0; k < steps; ++k)
-              umma_bf16(tmem + j * kRows, desc_mn(ra + s * kStage + k * 2048, 8192, 1024),
-                        desc_mn(pa + hf * 8192 + k * 2048, kPHalf, 1024), idesc_o, (u | hf | k) != 0);
-            umma_commit(&mi.empty[s]);
-            ++it;
+#pragma unroll 1
+            for (int c = 0; c < 9; ++c) {
+              if (!(ok = wait(&mi.full_s[rg.s], rg.phase))) break;
+              tc_fence_after();
+              const uint32_t a = r_lo + rg.s * (kStage >> 4), b = q_lo + c * (kQChunk >> 4);
+#pragma unroll
+              for (int k = 0; k < 4; ++k) umma_lo(tmem + kTmemS, a + 2 * k, b + 2 * k, idesc, (c | k) != 0, leader);
+              commit(&mi.empty_s[rg.s]);
+              rg.next();
+            }
+            if (!ok) break;
+            commit(&mi.s_full);
+            if (t == pc.n - 1) commit(&mi.q_empty);
           }
         }
-        umma_commit(&mi.pv_done);
-        return true;
-      };
-      done += pc.n;
-      for (int t = 0; t < pc.n && ok; ++t) {
-        const uint32_t nth = done - pc.n + t;
-        if (nth > 0 && !(ok = mbar_wait(&mi.s_empty, (nth - 1) & 1, wc))) break;
-        for (int c = 0; c < 9; ++c) {
-          const uint32_t s = it % kStages;
-          if (!(ok = mbar_wait(&mi.full[s], (it / kStages) & 1, wc))) break;
-          tc_fence_after();
-          const uint64_t ad = umma_desc_sw128(ra + s * kStage), bd = umma_desc_sw128(qa + c * kQChunk);
+      } else {
+        Ring<kVStages> rg;
+        uint32_t zph = 0;
+        const uint32_t v_lo = desc_lo(smem_u32(sRingV), 8192), p_lo = desc_lo(smem_u32(sP), kPHalf);   // MN-major
+        while (ok && walk.next(&pc)) {
+          const Group& g = pc.g;
+          if (g.ntok == 0) continue;
+          const uint32_t idesc = umma_idesc_bf16(128, (g.nrows + 15) / 16 * 16) | (1u << 15) | (1u << 16);
+          for (int t = 0; t < pc.n && ok; ++t, ++nth) {
+            const int v = tile_tokens(g, pc.t0 + t), halves = v > 64 ? 2 : 1;
+            const bool zero = !FP4 && pc.last && t == pc.n - 1 && (v & 15);
+            if (!(ok = wait(&mi.p_full, nth & 1))) break;
+            tc_fence_after();
+#pragma unroll 1
+            for (int j = 0; j < 4 && ok; ++j) {
+#pragma unroll 1
+              for (int hf = 0; hf < halves; ++hf) {
+                if (zero && hf == halves - 1) {
+                  if (!(ok = wait(&mi.zeroed[rg.s], (zph >> rg.s) & 1))) break;
+                  zph ^= 1u << rg.s;
+                }
+                if (!(ok = wait(&mi.full_v[rg.s], rg.phase))) break;
+                tc_fence_after();
+                const int left = v - 64 * hf;
+                const uint32_t a = v_lo + rg.s * (kStage >> 4), b = p_lo + hf * (8192 >> 4), d = tmem + j * kRows;
+                if (left >= 64) {
 #pragma unroll
-          for (int k = 0; k < 4; ++k) umma_bf16(tmem + kTmemS, ad + 2 * k, bd + 2 * k, idesc_s, (c | k) != 0);
-          umma_commit(&mi.empty[s]);
-          ++it;
+                  for (int k = 0; k < 4; ++k) umma_lo(d, a + k * 128, b + k * 128, idesc, (t | hf | k) != 0, leader);
+                } else {
+                  for (int k = 0; k < (left + 15) / 16; ++k)
+                    umma_lo(d, a + k * 128, b + k * 128, idesc, (t | hf | k) != 0, leader);
+                }
+                commit(&mi.empty_v[rg.s]);
+                rg.next();
+              }
+            }
+            if (ok) commit(&mi.pv_done);
+          }
         }
-        if (!ok) break;
-        umma_commit(&mi.s_full);
-        if (t == pc.n - 1) umma_commit(&mi.q_empty);
-        if (t > 0) ok = values(t - 1);
       }
-      if (ok) ok = values(pc.n - 1);
-    }
-    // every MMA has finished before TMEM is freed, on an early exit too (bounded)
-    umma_commit(&mi.mma_done);
-    const uint64_t t0 = global_timer_ns();
-    while (!mbar_try_wait(smem_u32(&mi.mma_done), 0) && global_timer_ns() - t0 <= kDrainNs) {
-    }
+      // every MMA has finished before TMEM is freed, on an early exit too (bounded)
+      commit(&mi.mma_done);
+      const uint64_t t0 = global_timer_ns();
+      while (!mbar_try_wait(smem_u32(&mi.mma_done), 0) && global_timer_ns() - t0 <= kDrainNs) {
+      }
     }
     __syncwarp();
   }
@@ -969,8 +1093,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 }
 
 // ---------------------------------------------------------------- merge
-// Block (i, r): row r of the group that block i's share leaves unfinished, from its pieces in
-// the order of their tiles; with malformed offsets, rows of the call as attending to nothing.
+// Rows of the groups that several blocks share, from the pieces in the order of their tiles, a
+// block of threads a row at a time; with malformed offsets, rows of the call as attending to nothing.
 constexpr int kMergeThreads = 128;
 
 // Row `row` of out from its own prefix alone, by the block: scores of 128 tokens at a time, a
@@ -1022,85 +1146,60 @@ __device__ void redo_row(const Params& p, int64_t row) {
 }
 
 __global__ void __launch_bounds__(kMergeThreads) latent_merge_kernel(Params p, int blocks) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const Ws& w = p.ws;
   const int tid = threadIdx.x;
-  if (w.plan->bad) {
+  const Plan plan = *w.plan;
+  if (plan.bad) {
     const int64_t rows = static_cast<int64_t>(p.T) * p.H;
-    const int64_t nb = static_cast<int64_t>(gridDim.x) * gridDim.y;
-    for (int64_t r = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x; r < rows; r += nb) {
+    for (int64_t r = blockIdx.x; r < rows; r += gridDim.x) {
       reinterpret_cast<uint2*>(p.out + r * kLatV)[tid] = make_uint2(0u, 0u);
       if (tid == 0) p.lse[r] = -INFINITY;
     }
     return;
   }
-  {
-    const int64_t nb = static_cast<int64_t>(gridDim.x) * gridDim.y;
-    for (int64_t k = static_cast<int64_t>(blockIdx.y) * gridDim.x + blockIdx.x; k < w.plan->spoiled; k += nb)
-      redo_row(p, w.spoiled[k]);
-  }
-  const int i = blockIdx.x;
-  int64_t a, b;
-  share(w.plan->tiles, i, blocks, &a, &b);
-  if (a >= b) return;
-  // the last group of the share, if it starts in it and goes on behind it
-  int lo = 0, hi = w.plan->groups - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (w.tile0[mid] < b) lo = mid;
-    else hi = mid - 1;
-  }
-  const int64_t end = w.tile0[lo + 1];
-  if (end <= b || w.tile0[lo] < a) return;
-  const Group g = w.group[lo];
-  const int r = blockIdx.y;
-  if (r >= g.nrows) return;
-  int last = i;      // the block that holds the group's last tile
-  {
-    int l2 = i, h2 = blocks - 1;
-    while (l2 < h2) {
-      const int mid = (l2 + h2) >> 1;
+  for (int k = blockIdx.x; k < plan.spoiled; k += gridDim.x) redo_row(p, w.spoiled[k]);
+  for (int item = blockIdx.x; item < plan.merges * kRows; item += gridDim.x) {
+    const Merge mg = w.merge[item / kRows];
+    const int r = item % kRows;
+    if (r >= mg.nrows) continue;
+    // pieces: the tail slot of the first block, then the head slots of the others (a block with an
+    // empty share, where there are fewer tiles than blocks, has none)
+    float m = kUnset;
+    for (int k = mg.first; k <= mg.last; ++k) {
       int64_t x, y;
-      share(w.plan->tiles, mid, blocks, &x, &y);
-      if (y >= end) h2 = mid;
-      else l2 = mid + 1;
+      share(plan.tiles, k, blocks, &x, &y);
+      if (x >= y) continue;
+      const float2 v = w.ml[static_cast<int64_t>(2 * k + (k == mg.first)) * kRows + r];
+      if (v.y != 0.f) m = fmaxf(m, v.x);
     }
-    last = l2;
-  }
-  // pieces: the tail slot of block i, then the head slots of the blocks up to `last` (a block
-  // without tiles, between shares, has none: its m and l are skipped by its empty share)
-  float m = kUnset;
-  for (int k = i; k <= last; ++k) {
-    int64_t x, y;
-    share(w.plan->tiles, k, blocks, &x, &y);
-    if (x >= y) continue;
-    const float2 v = w.ml[static_cast<int64_t>(2 * k + (k == i)) * kRows + r];
-    if (v.y != 0.f) m = fmaxf(m, v.x);
-  }
-  float l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-  for (int k = i; k <= last; ++k) {
-    int64_t x, y;
-    share(w.plan->tiles, k, blocks, &x, &y);
-    if (x >= y) continue;
-    const int64_t slot = 2 * k + (k == i);
-    const float2 v = w.ml[slot * kRows + r];
-    const float4 c = reinterpret_cast<const float4*>(w.o + slot * kSlotFloats + static_cast<int64_t>(r) * kLatV)[tid];
-    if (v.y != 0.f) {
-      const float f = ex2_approx(v.x - m);
-      l = fmaf(v.y, f, l);
-      o.x = fmaf(c.x, f, o.x);
-      o.y = fmaf(c.y, f, o.y);
-      o.z = fmaf(c.z, f, o.z);
-      o.w = fmaf(c.w, f, o.w);
+    for (int k = mg.first; k <= mg.last; ++k) {
+      int64_t x, y;
+      share(plan.tiles, k, blocks, &x, &y);
+      if (x >= y) continue;
+      const int64_t slot = 2 * k + (k == mg.first);
+      const float2 v = w.ml[slot * kRows + r];
+      const float4 c = reinterpret_cast<const float4*>(w.o + slot * kSlotFloats + static_cast<int64_t>(r) * kLatV)[tid];
+      if (v.y != 0.f) {
+        const float f = ex2_approx(v.x - m);
+        l = fmaf(v.y, f, l);
+        o.x = fmaf(c.x, f, o.x);
+        o.y = fmaf(c.y, f, o.y);
+        o.z = fmaf(c.z, f, o.z);
+        o.w = fmaf(c.w, f, o.w);
+      }
     }
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+    const int64_t row = mg.row0 + r;
+    reinterpret_cast<uint2*>(p.out + row * kLatV)[tid] =
+        l != 0.f ? make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv)) : make_uint2(0u, 0u);
+    if (tid == 0) p.lse[row] = l != 0.f ? fmaf(m, 0.69314718055994531f, logf(l)) : -INFINITY;
+    const bool nan = l == l && l != 0.f && !(o.x == o.x && o.y == o.y && o.z == o.z && o.w == o.w);
+    if (p.kv && __syncthreads_or(nan)) redo_row(p, row);
   }
-  const float inv = l != 0.f ? 1.f / l : 0.f;
-  const int64_t row = g.row0 + r;
-  reinterpret_cast<uint2*>(p.out + row * kLatV)[tid] =
-      l != 0.f ? make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv)) : make_uint2(0u, 0u);
-  if (tid == 0) p.lse[row] = l != 0.f ? fmaf(m, 0.69314718055994531f, logf(l)) : -INFINITY;
-  if (p.kv && __syncthreads_or(l == l && l != 0.f && !(o.x == o.x && o.y == o.y && o.z == o.z && o.w == o.w))) redo_row(p, row);
 }
 
 }  // namespace
@@ -1134,10 +1233,24 @@ cudaError_t launch_latent_attention(const LatentArgs& a, const CUtensorMap& tmQ,
   auto kern = a.fp4 ? latent_attention_kernel<true> : latent_attention_kernel<false>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;
-  latent_plan_kernel<<<1, kPlanThreads, 0, s>>>(p);
-  kern<<<blocks, kThreads, kSmem, s>>>(tmQ, tmC, p);
-  latent_merge_kernel<<<dim3(blocks, kRows), kMergeThreads, 0, s>>>(p, blocks);
-  return cudaGetLastError();
+  // the later two start while their predecessor runs out and wait for its results themselves
+  latent_plan_kernel<<<1, kPlanThreads, 0, s>>>(p, blocks);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  cudaLaunchAttribute dep;
+  dep.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  dep.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(a.fp4 ? Roles<true>::kThreads : Roles<false>::kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  cfg.stream = s;
+  cfg.attrs = &dep;
+  cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, kern, tmQ, tmC, p)) != cudaSuccess) return e;
+  cfg.gridDim = dim3(16 * blocks);
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, latent_merge_kernel, p, blocks);
 }
 
 }  // namespace dsa

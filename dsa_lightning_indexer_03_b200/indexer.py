@@ -6,6 +6,7 @@ torch supplies device memory and the CUDA stream; every step of the indexer
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 
 import torch
@@ -301,9 +302,13 @@ class Indexer:
         return t
 
     def _on(self, stream):
-        """The stream of a call, current for its allocations (torch's allocator then reuses its
-        workspace only behind the call)."""
-        return torch.cuda.stream(torch.cuda.current_stream(self.device) if stream is None else stream)
+        """The stream of a call, and its device, current for its allocations (torch's allocator then
+        reuses its workspace only behind the call).  Nothing to switch costs nothing."""
+        if stream is None:
+            if torch.cuda.current_device() == self.device.index:
+                return contextlib.nullcontext()
+            return torch.cuda.device(self.device)
+        return torch.cuda.stream(stream)
 
     def _latent(self, q, kv, fp4, positions, q_seq_offsets, cache_offsets, scale, idx, out, lse, stream):
         T, H, B = self._latent_common(q, 576, positions, q_seq_offsets, cache_offsets, kv,
@@ -316,7 +321,7 @@ class Indexer:
             k_sel = idx.shape[1]
         elif positions is None:
             raise ValueError("positions are needed without idx")
-        with torch.cuda.device(self.device), self._on(stream):
+        with self._on(stream):
             out = self._out(out, "out", torch.bfloat16, (T, H, 512))
             lse = self._out(lse, "lse", torch.float32, (T, H))
             n = self._lib.dsa_indexer_latent_attention_workspace(self._h, T, B, H)
@@ -358,7 +363,7 @@ class Indexer:
             _need(rows, "rows", torch.int64, dev)
             if rows.shape != (n,) or out is None:
                 raise ValueError("rows must be [n] and come with out")
-        with torch.cuda.device(dev), self._on(stream):
+        with self._on(stream):
             if out is None:
                 out = torch.empty((n, 416), dtype=torch.uint8, device=dev)
             _need(out, "out", torch.uint8, dev)
@@ -380,7 +385,7 @@ class Indexer:
             if rows.dim() != 1:
                 raise ValueError("rows must be [n]")
         n = kv_fp4.shape[0] if rows is None else rows.numel()
-        with torch.cuda.device(dev), self._on(stream):
+        with self._on(stream):
             out = self._out(out, "out", torch.bfloat16, (n, 576))
             check(self._lib.dsa_indexer_dequantize_latent_fp4(self._h, n, _ptr(kv_fp4), kv_fp4.shape[0], _ptr(rows),
                                                               _ptr(out), _stream(None)),
@@ -398,7 +403,7 @@ class Indexer:
             raise ValueError("W_ukv must be [H, 256, 512]")
         if positions is None:
             raise ValueError("positions are needed")
-        with torch.cuda.device(self.device), self._on(stream):
+        with self._on(stream):
             out = self._out(out, "out", torch.bfloat16, (T, H, 128))
             n = self._lib.dsa_indexer_latent_expanded_workspace(self._h, T, B, H, kv_cache.shape[0])
             ws = torch.empty(max(n, 16), dtype=torch.uint8, device=self.device)
