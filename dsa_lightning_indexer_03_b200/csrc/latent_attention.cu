@@ -318,11 +318,6 @@ __device__ __forceinline__ void umma_lo(uint32_t d, uint32_t a_lo, uint32_t b_lo
       : "memory");
 }
 
-// fetch of `bytes` (a multiple of 16) from a 16-byte aligned address into L2
-__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
-  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
-}
-
 // position in a ring of N stages and the parity of its full barriers
 template <int N>
 struct Ring {
@@ -590,6 +585,10 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
       while (!mbar_try_wait(smem_u32(bar), parity) && global_timer_ns() - t0 <= kDrainNs) {
       }
     };
+    // L2 keeps a tile between its two readings: without these hints 1.8 times the cache's bytes came
+    // from memory (64 sequences of 8,192 tokens), and the decode batch of 64 took 1.81 ms, not 1.44.
+    // Fetching the next tile into L2 as well made room for less of that and took 1.58 ms.
+    const uint64_t keep = l2_policy_evict_last(), drop = l2_policy_evict_first();
     uint32_t it = 0;        // stages of the warp's ring so far
     uint32_t segs = 0;      // pieces so far
     bool ok = true;
@@ -687,8 +686,7 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
       }
       if (scores && i == 0 && !ok && segs > 0) drain(&mi.q_full, (segs - 1) & 1);
     } else if (warp == 0 && lane == 0) {
-      // scores: nine 64-value chunks of a tile; the next tile is fetched into L2 meanwhile, since
-      // the ring alone holds less than the memory's latency asks for
+      // scores: nine 64-value chunks of a tile
       while (ok && walk.next(&pc)) {
         if (pc.g.ntok == 0) continue;
         ok = q_load();
@@ -696,17 +694,13 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
         for (int t = pc.t0; t < pc.t0 + pc.n && ok; ++t) {
           const bool two = tile_tokens(pc.g, t) > 64;
           const int y = static_cast<int>(pc.g.kv_row0) + t * kTile;
-          // bytes of the next tile, fetched in order (rows follow one another, while a stage's loads
-          // touch 128 bytes of each)
-          const int ahead = t + 1 < pc.t0 + pc.n ? tile_tokens(pc.g, t + 1) * 2 * kLatDim : 0;
-          const uint8_t* const src = reinterpret_cast<const uint8_t*>(p.kv + static_cast<int64_t>(y + kTile) * kLatDim);
           for (int c = 0; c < 9; ++c) {
             if (!(ok = acquire(mi.empty_s, it, kSStages))) break;
             const uint32_t s = it % kSStages;
             mbar_arrive_expect_tx(&mi.full_s[s], two ? kStage : kStage / 2);
-            tma_load_2d(sRing + s * kStage, &tmC, &mi.full_s[s], 64 * c, y);
-            if (two) tma_load_2d(sRing + s * kStage + kStage / 2, &tmC, &mi.full_s[s], 64 * c, y + 64);
-            if (ahead > c * kStage) prefetch_l2(src + c * kStage, ahead - c * kStage < kStage ? ahead - c * kStage : kStage);
+            const uint64_t pol = c < 8 ? keep : drop;
+            tma_load_2d_hint(sRing + s * kStage, &tmC, &mi.full_s[s], 64 * c, y, pol);
+            if (two) tma_load_2d_hint(sRing + s * kStage + kStage / 2, &tmC, &mi.full_s[s], 64 * c, y + 64, pol);
             ++it;
           }
         }
@@ -728,8 +722,8 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
             if (!(ok = acquire(mi.empty_v, it, kVStages))) break;
             const uint32_t s = it % kVStages;
             mbar_arrive_expect_tx(&mi.full_v[s], kStage);
-            tma_load_2d(sRingV + s * kStage, &tmC, &mi.full_v[s], 128 * j, y);
-            tma_load_2d(sRingV + s * kStage + kStage / 2, &tmC, &mi.full_v[s], 128 * j + 64, y);
+            tma_load_2d_hint(sRingV + s * kStage, &tmC, &mi.full_v[s], 128 * j, y, drop);
+            tma_load_2d_hint(sRingV + s * kStage + kStage / 2, &tmC, &mi.full_v[s], 128 * j + 64, y, drop);
             if (hf == halves - 1 && (v & 15)) mbar_arrive(&mi.zero_req[s]);
             ++it;
           }
