@@ -18,7 +18,7 @@ LIB_NAME = "libdsa_indexer.so"
 LIB_PATH = os.path.join(PKG_DIR, LIB_NAME)
 SOURCES = ["api.cu", "proj.cu", "score_topk.cu", "noalloc.cu", "reuse.cu", "sparse_mla.cu", "latent_fp4.cu",
            "latent_attention.cu", "latent_expanded.cu"]
-HEADERS = ["common.cuh", "kernels.h", "latent.h"]
+HEADERS = ["common.cuh", "kernels.h", "latent.h", "latent_mma.cuh"]
 # the sources of the kernels whose profile figures are recorded under source_hash()
 PROFILED = ["proj.cu", "score_topk.cu", "noalloc.cu", "reuse.cu", "sparse_mla.cu", "common.cuh", "kernels.h"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]

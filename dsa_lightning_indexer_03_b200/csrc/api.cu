@@ -581,7 +581,7 @@ int64_t dsa_indexer_latent_expanded_workspace(dsa_indexer_t h, int64_t T, int32_
   if (!h || T < 0 || B < 1 || n_heads < 1 || n_heads > 1024 || T > (int64_t(1) << 30) || T * n_heads > (int64_t(1) << 30) || cache_rows < 1 ||
       cache_rows > 65535 * int64_t(128))
     return -1;
-  return expanded_plan_bytes(T, B, n_heads, h->num_sms) + cache_rows * n_heads * 512;
+  return expanded_workspace_bytes(T, B, n_heads, cache_rows, h->num_sms);
 }
 
 dsa_status_t dsa_indexer_latent_attention_expanded(dsa_indexer_t h, int64_t T, const void* q, int32_t n_heads,
@@ -594,18 +594,11 @@ dsa_status_t dsa_indexer_latent_attention_expanded(dsa_indexer_t h, int64_t T, c
   if (st != DSA_OK || T == 0) return st;
   if (!positions || !W_ukv || !aligned16(W_ukv)) return DSA_ERR_INVALID_ARG;
   if (cache_rows > 65535 * int64_t(128)) return DSA_ERR_UNSUPPORTED;
-  const int64_t plan = expanded_plan_bytes(T, B, n_heads, h->num_sms);
-  if (workspace_bytes < plan + cache_rows * n_heads * 512) return DSA_ERR_WORKSPACE;
-  __nv_bfloat16* const kv_exp = reinterpret_cast<__nv_bfloat16*>(static_cast<uint8_t*>(workspace) + plan);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  // keys and values of every cache row: [rows, 512] x W_ukv^T -> [rows, H * 256]
+  if (workspace_bytes < expanded_workspace_bytes(T, B, n_heads, cache_rows, h->num_sms)) return DSA_ERR_WORKSPACE;
   CUtensorMap tmC, tmW;
   if (!make_tmap(&tmC, kv_cache, kLatV, uint64_t(cache_rows), 64, 128, false, kLatDim) ||
       !make_tmap(&tmW, W_ukv, kLatV, uint64_t(n_heads) * 256, 64, 256))
     return DSA_ERR_INVALID_ARG;
-  if (launch_proj_q(tmC, tmW, static_cast<int>(cache_rows), kLatV, n_heads * 256, kv_exp, h->ws.err, timeout_ns(), s) !=
-      cudaSuccess)
-    return DSA_ERR_CUDA;
   ExpandedArgs a;
   a.T = static_cast<int>(T);
   a.B = B;
@@ -613,17 +606,16 @@ dsa_status_t dsa_indexer_latent_attention_expanded(dsa_indexer_t h, int64_t T, c
   a.cache_rows = cache_rows;
   a.q = q;
   a.kv = kv_cache;
-  a.kv_exp = kv_exp;
   a.positions = positions;
   a.q_seq_offsets = q_seq_offsets;
   a.cache_offsets = cache_offsets;
   a.scale = scale;
   a.out = out;
-  a.plan = workspace;
+  a.workspace = workspace;
   a.num_sms = h->num_sms;
   a.err = h->ws.err;
   a.timeout_ns = timeout_ns();
-  return launch_latent_expanded(a, s) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
+  return launch_latent_expanded(a, tmC, tmW, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DSA_OK : DSA_ERR_CUDA;
 }
 
 dsa_status_t dsa_indexer_device_error(dsa_indexer_t h) {

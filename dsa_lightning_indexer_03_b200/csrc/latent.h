@@ -55,26 +55,27 @@ cudaError_t launch_quantize_latent_fp4(int64_t n, const void* kv, const int64_t*
 cudaError_t launch_dequantize_latent_fp4(int64_t n, const uint8_t* kv4, int64_t kv_rows, const int64_t* rows, void* out,
                                          int* err, int num_sms, cudaStream_t s);
 
-// Attention in the expanded form: q [T, H, 192] against keys [cache_rows, H, 256] expanded
-// from the latent (128 key values, then 128 values) and the shared 64-value rope key of kv.
+// Attention in the expanded form: q [T, H, 192] against the keys (128 + 64 values) and values
+// (128) that W_ukv expands from the latent.
 struct ExpandedArgs {
   int T, B, H;
   int64_t cache_rows;
   const void* q;                  // bf16 [T, H, 192]
   const void* kv;                 // bf16 [cache_rows, 576]
-  const void* kv_exp;             // bf16 [cache_rows, H, 256]
   const int32_t* positions;
   const int32_t* q_seq_offsets;
   const int64_t* cache_offsets;
   float scale;
   void* out;                      // bf16 [T, H, 128]
-  void* plan;                     // workspace of the plan
+  void* workspace;
   int num_sms;
   int* err;
   uint64_t timeout_ns;
 };
 
-int64_t expanded_plan_bytes(int64_t T, int64_t B, int64_t H, int num_sms);
-cudaError_t launch_latent_expanded(const ExpandedArgs& a, cudaStream_t s);
+int64_t expanded_workspace_bytes(int64_t T, int64_t B, int64_t H, int64_t cache_rows, int num_sms);
+// tmC: the latents of the cache [cache_rows, 512] (rows 576 values apart), boxes of 64 values x 128
+// rows; tmW: W_ukv [H * 256, 512], boxes of 64 values x 256 rows
+cudaError_t launch_latent_expanded(const ExpandedArgs& a, const CUtensorMap& tmC, const CUtensorMap& tmW, cudaStream_t s);
 
 }  // namespace dsa

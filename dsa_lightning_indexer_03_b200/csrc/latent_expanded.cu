@@ -5,96 +5,1088 @@
 //   x[t,h,s] = scale * (q[t,h][0..127] . k[s,h] + q[t,h][128..191] . c[s][512..575]),
 //   out[t,h] = sum_s softmax_s(x) * v[s,h].
 //
-// First form: one warp per (token, head), an online softmax over the prefix.
+// Keys, values and weights are held in fp16: as bf16 their three roundings of up to 2^-8 would
+// triple the error that rounding out to bf16 leaves, in fp16 (2^-11 each) they add 2% to it.
+// fp16's range is met by powers of two, which round nothing: a scale for each query row (taken
+// out of q), and for each 128 tokens of a head one for its keys and one for its values, set by
+// the largest magnitude.  The softmax then works on x + fv, fv the exponent of the tile's value
+// scale, so that the weights it hands to the product carry that scale; sums divide it out again.
+//
+// up_project_kernel: keys and values of every (128 tokens, head), [128, 512] x W_h^T [512, 256],
+//   written as the 128-byte-swizzled images that the attention's MMAs read, so that it fetches
+//   them with plain bulk copies.  One block per SM, the tokens' latents stay in shared memory
+//   for all heads, W streams through a ring, and the epilogue of a head (8 warps) runs under
+//   the MMAs of the next (two accumulators of 256 TMEM columns).
+// expanded_kernel: one block of 20 warps per SM.  An item is (256 queries, head): two tiles of
+//   128 rows, whose scores (128 columns each) and sums (128) fill TMEM.  One warp issues the MMAs
+//   of a tile, so that the tensor core works on one tile while the softmax of the other runs;
+//   two warpgroups do that softmax, a thread for half of a row (64 tokens).  The weights
+//   replace the scores in TMEM (the A operand of the second product).  K and V of 128 tokens
+//   are 80 KB, read once for both tiles, through rings of four 16 KB and two 32 KB stages.
+//   Items are taken in order from a counter, longest first among a sequence's; the heads go in
+//   groups whose keys and values fit L2.  When there are too few items for that to balance,
+//   every block takes an equal share of all 128-token steps instead, and merge_expanded_kernel
+//   joins the pieces of an item.
+//
+// Bound: the tensor core, 128 x 128 x (192 + 128) products in 1,280 cycles, and close behind
+// it the 16,384 exponentials of those weights (1,024 cycles).
+
+#include <cuda_fp16.h>
 
 #include "latent.h"
+#include "latent_mma.cuh"
 
 namespace dsa {
 namespace {
 
-constexpr int kWarps = 8;
+constexpr int kTok = 128;                     // tokens of a step
+constexpr int kRowsT = 128;                   // query rows of a tile
+constexpr int kPair = 2 * kRowsT;
+constexpr int kChunk = 16384;                 // 128 rows x 64 fp16
+constexpr int kKvBytes = 5 * kChunk;          // keys (three chunks), then values (two), of 128 tokens
+constexpr uint64_t kDrainNs = 200ull * 1000 * 1000;
+constexpr float kUnset = -1e38f;              // reference of a row without a token so far
+constexpr float kLift = 7.f;                  // weights reach 2^(8 + 7): the upper end of fp16's range
+constexpr int64_t kL2Bytes = 48ll << 20;      // keys and values that a group of heads may take
 
-__device__ __forceinline__ float bf_lo(uint32_t u) { return __uint_as_float(u << 16); }
-__device__ __forceinline__ float bf_hi(uint32_t u) { return __uint_as_float(u & 0xFFFF0000u); }
+struct Pair {           // up to 256 queries of a sequence
+  int64_t kv_row0;      // cache row of the sequence's token 0
+  int32_t tok0, ntok;   // first query, number of queries
+  int32_t tile0;        // the sequence's first 128-token step among all
+  int32_t seq_len;
+  int32_t n[2];         // steps of either tile of rows
+};
 
-__global__ void check_offsets_kernel(ExpandedArgs a, int* bad) {
-  int b_bad = 0;
-  for (int b = threadIdx.x; b < a.B; b += blockDim.x) {
-    const int64_t q0 = a.q_seq_offsets[b], q1 = a.q_seq_offsets[b + 1];
-    const int64_t c0 = a.cache_offsets[b], c1 = a.cache_offsets[b + 1];
-    if (q0 < 0 || q1 < q0 || q1 > a.T || c0 < 0 || c1 < c0 || c1 > a.cache_rows) b_bad = 1;
+struct Steps {          // 128 tokens to expand
+  int32_t row0, valid;  // first cache row, rows that some query attends to
+};
+
+struct Plan {
+  int32_t pairs, tiles;     // entries of Ws::pair and Ws::step
+  int64_t steps;            // over all pairs, of one head
+  int32_t bad, merges;
+  int32_t next, pad;
+};
+
+struct Merge {
+  int32_t pair, head, first, last;   // an item in the shares of several blocks
+};
+
+struct Ws {
+  Plan* plan;
+  int32_t* seq_pair;    // [B+1] first pair of each sequence
+  int32_t* seq_tile;    // [B+1] first step of each sequence
+  int32_t* used;        // [B] tokens that some query attends to
+  Pair* pair;           // [max pairs]
+  int64_t* step0;       // [max pairs + 1] steps before each pair
+  Steps* step;          // [max tiles]
+  Merge* merge;         // [blocks]
+  float2* scale;        // [max tiles][H] exponents of the key and value scales
+  float2* ml;           // [2 * blocks][256] reference and sum of a piece's rows
+  float* o;             // [2 * blocks][256][128]
+  uint8_t* kv;          // [max tiles][H][kKvBytes]
+  int64_t max_pairs, max_tiles, bytes;
+};
+
+Ws carve(void* base, int64_t T, int64_t B, int64_t H, int64_t cache_rows, int blocks) {
+  Ws w;
+  w.max_pairs = T / kPair + (B < T ? B : T) + 1;
+  w.max_tiles = cache_rows / kTok + (B < T ? B : T) + 1;
+  int64_t off = 0;
+  auto take = [&](int64_t bytes) {
+    uint8_t* p = static_cast<uint8_t*>(base) + off;
+    off = (off + bytes + 255) & ~int64_t(255);
+    return p;
+  };
+  w.plan = reinterpret_cast<Plan*>(take(sizeof(Plan)));
+  w.seq_pair = reinterpret_cast<int32_t*>(take(4 * (B + 1)));
+  w.seq_tile = reinterpret_cast<int32_t*>(take(4 * (B + 1)));
+  w.used = reinterpret_cast<int32_t*>(take(4 * B));
+  w.pair = reinterpret_cast<Pair*>(take(sizeof(Pair) * w.max_pairs));
+  w.step0 = reinterpret_cast<int64_t*>(take(8 * (w.max_pairs + 1)));
+  w.step = reinterpret_cast<Steps*>(take(sizeof(Steps) * w.max_tiles));
+  w.merge = reinterpret_cast<Merge*>(take(sizeof(Merge) * blocks));
+  w.scale = reinterpret_cast<float2*>(take(sizeof(float2) * w.max_tiles * H));
+  w.ml = reinterpret_cast<float2*>(take(sizeof(float2) * kPair * 2 * blocks));
+  w.o = reinterpret_cast<float*>(take(int64_t(4) * kPair * 128 * 2 * blocks));
+  w.kv = take(w.max_tiles * H * kKvBytes);
+  w.bytes = off;
+  return w;
+}
+
+struct Params {
+  int T, B, H;
+  bool split;                   // equal shares of all steps instead of whole items
+  int64_t cache_rows;
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* kv;
+  const int32_t* positions;
+  const int32_t* q_seq_offsets;
+  const int64_t* cache_offsets;
+  float scale_log2;
+  __nv_bfloat16* out;
+  Ws ws;
+  int* err;
+  uint64_t timeout_ns;
+};
+
+// the last b with first[b] <= x, of n entries
+__device__ __forceinline__ int last_at(const int32_t* first, int n, int x) {
+  int lo = 0, hi = n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (first[mid] <= x) lo = mid;
+    else hi = mid - 1;
   }
-  b_bad = __syncthreads_or(b_bad);
-  if (threadIdx.x == 0) {
-    *bad = b_bad;
-    if (b_bad) atomicOr(a.err, kErrOffsets);
+  return lo;
+}
+
+// ---------------------------------------------------------------- plan
+__global__ void __launch_bounds__(kPlanThreads) expanded_plan_kernel(Params p, int blocks) {
+  asm volatile("griddepcontrol.launch_dependents;");
+  __shared__ int64_t sums[32];
+  const Ws& w = p.ws;
+  const int tid = threadIdx.x, lane = tid & 31;
+  int bad = 0;
+  for (int b = tid; b < p.B; b += kPlanThreads) {
+    const int64_t q0 = p.q_seq_offsets[b], q1 = p.q_seq_offsets[b + 1];
+    const int64_t c0 = p.cache_offsets[b], c1 = p.cache_offsets[b + 1];
+    if (q0 < 0 || q1 < q0 || q1 > p.T || c0 < 0 || c1 < c0 || c1 > p.cache_rows) bad = 1;
+    w.used[b] = 0;
+  }
+  bad = __syncthreads_or(bad);
+  if (bad) {   // the attention kernel writes every row as attending to nothing
+    if (tid == 0) {
+      *w.plan = Plan{0, 0, 0, 1, 0, 0, 0};
+      atomicOr(p.err, kErrOffsets);
+    }
+    return;
+  }
+  int base = 0;
+  for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
+    const int b = b0 + tid;
+    const int n = b < p.B ? (p.q_seq_offsets[b + 1] - p.q_seq_offsets[b] + kPair - 1) / kPair : 0;
+    const int inc = static_cast<int>(block_scan(n, sums));
+    if (b < p.B) w.seq_pair[b + 1] = base + inc;
+    base += static_cast<int>(sums[31]);
+  }
+  if (tid == 0) w.seq_pair[0] = 0;
+  __syncthreads();
+  const int pairs = base;
+  // a warp per pair: its queries and the steps of its two tiles; a sequence's pairs in reverse
+  // (with positions that rise, the longest first)
+  int oob = 0;
+  for (int k = tid >> 5; k < pairs; k += kPlanThreads / 32) {
+    const int b = last_at(w.seq_pair, p.B, k);
+    const int q0 = p.q_seq_offsets[b], q1 = p.q_seq_offsets[b + 1];
+    const int i = w.seq_pair[b + 1] - 1 - k;     // counted from the sequence's first queries
+    Pair pr;
+    pr.kv_row0 = p.cache_offsets[b];
+    pr.seq_len = static_cast<int32_t>(p.cache_offsets[b + 1] - pr.kv_row0);
+    pr.tok0 = q0 + i * kPair;
+    pr.ntok = q1 - pr.tok0 < kPair ? q1 - pr.tok0 : kPair;
+    pr.tile0 = b;                                // replaced below
+    int top = -1;
+    for (int hf = 0; hf < 2; ++hf) {
+      int m = -1;
+      for (int j = hf * kRowsT + lane; j < (hf + 1) * kRowsT && j < pr.ntok; j += 32) {
+        const int pos = p.positions[pr.tok0 + j];
+        if (pos < -1 || pos >= pr.seq_len) oob = 1;
+        else m = pos > m ? pos : m;
+      }
+      m = __reduce_max_sync(0xffffffffu, m);
+      pr.n[hf] = (m + kTok) / kTok;
+      top = m > top ? m : top;
+    }
+    if (lane == 0) {
+      w.pair[k] = pr;
+      atomicMax(&w.used[b], top + 1);
+    }
+  }
+  if (oob) atomicOr(p.err, kErrBounds);
+  __syncthreads();
+  base = 0;
+  for (int b0 = 0; b0 < p.B; b0 += kPlanThreads) {
+    const int b = b0 + tid;
+    const int n = b < p.B ? (w.used[b] + kTok - 1) / kTok : 0;
+    const int inc = static_cast<int>(block_scan(n, sums));
+    if (b < p.B) w.seq_tile[b + 1] = base + inc;
+    base += static_cast<int>(sums[31]);
+  }
+  if (tid == 0) w.seq_tile[0] = 0;
+  __syncthreads();
+  const int tiles = base;
+  for (int k = tid; k < tiles; k += kPlanThreads) {
+    const int b = last_at(w.seq_tile, p.B, k), j = (k - w.seq_tile[b]) * kTok;
+    const int left = w.used[b] - j;
+    w.step[k] = Steps{static_cast<int32_t>(p.cache_offsets[b] + j), left < kTok ? left : kTok};
+  }
+  int64_t steps = 0;
+  for (int k0 = 0; k0 < pairs; k0 += kPlanThreads) {
+    const int k = k0 + tid;
+    int n = 0;
+    if (k < pairs) {
+      Pair& pr = w.pair[k];
+      pr.tile0 = w.seq_tile[pr.tile0];
+      n = pr.n[0] > pr.n[1] ? pr.n[0] : pr.n[1];
+      if (n == 0) n = 1;                         // a pair without tokens still writes its rows
+    }
+    const int64_t inc = block_scan(n, sums);
+    if (k < pairs) w.step0[k] = steps + inc - n;
+    steps += sums[31];
+  }
+  if (tid == 0) w.step0[pairs] = steps;
+  int* const count = reinterpret_cast<int*>(sums);
+  __syncthreads();
+  if (tid == 0) *count = 0;
+  __syncthreads();
+  if (p.split) {
+    const int64_t all = steps * p.H;
+    for (int64_t it = tid; it < static_cast<int64_t>(pairs) * p.H; it += kPlanThreads) {
+      const int h = static_cast<int>(it / pairs), k = static_cast<int>(it % pairs);
+      const int first = share_of(all, h * steps + w.step0[k], blocks), last = share_of(all, h * steps + w.step0[k + 1] - 1, blocks);
+      if (first != last) w.merge[atomicAdd(count, 1)] = Merge{k, h, first, last};
+    }
+  }
+  __syncthreads();
+  if (tid == 0) *w.plan = Plan{pairs, tiles, steps, 0, *count, 0, 0};
+}
+
+// ---------------------------------------------------------------- helpers
+// kind::f16 with fp16 A and B, fp32 accumulator, both K-major
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// 2^e, e in [-126, 127]
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+// Exponent f of the scale 2^f that brings a largest magnitude of `top` to below 2^15, so that
+// fp16 holds it; nothing is lifted by more than 2^14.
+__device__ __forceinline__ int scale_exponent(float top) {
+  const int e = static_cast<int>((__float_as_uint(top) >> 23) & 0xFF) - 127;
+  return (e < 0 ? 0 : e) - 14;
+}
+
+// |v|, or 0 for NaN and infinities (they stay what they are under any scale)
+__device__ __forceinline__ float finite_abs(float v) {
+  const float a = fabsf(v);
+  return a <= 3.4028235e38f ? a : 0.f;
+}
+
+// D (+)= A[tmem] . B[smem] by the elected lane
+__device__ __forceinline__ void umma_ta(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t idesc, bool accumulate,
+                                        bool leader) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
+      "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+      "mov.b64 b, {%2, %3};\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n\t}" ::"r"(d),
+      "r"(a_tmem), "r"(b_lo), "r"(kDescHi), "r"(idesc), "r"((uint32_t)accumulate), "r"((uint32_t)leader)
+      : "memory");
+}
+
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                   smem_u32(dst)),
+               "l"(src), "r"(bytes), "r"(smem_u32(bar))
+               : "memory");
+}
+
+__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(smem_u32(bar), parity) && global_timer_ns() - t0 <= kDrainNs) {
   }
 }
 
-__global__ void __launch_bounds__(kWarps * 32) expanded_simple_kernel(ExpandedArgs a, const int* bad) {
-  const int lane = threadIdx.x & 31;
-  const int64_t r = static_cast<int64_t>(blockIdx.x) * kWarps + (threadIdx.x >> 5);
-  if (r >= static_cast<int64_t>(a.T) * a.H) return;
-  const int t = static_cast<int>(r / a.H), h = static_cast<int>(r % a.H);
-  int64_t row0 = 0;
-  int n = 0;
-  if (!*bad) {
-    if (t < a.q_seq_offsets[0] || t >= a.q_seq_offsets[a.B]) return;   // a token of no sequence
-    int lo = 0, hi = a.B - 1;
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if (a.q_seq_offsets[mid] <= t) lo = mid;
-      else hi = mid - 1;
+// ---------------------------------------------------------------- keys and values
+constexpr int kUpStages = 3, kUpStage = 32768;      // 256 rows of W x 64 values
+constexpr int kUpA = 8 * kChunk;                    // the latents of 128 tokens
+constexpr int kUpThreads = 12 * 32;
+
+struct UpMisc {
+  uint64_t full[kUpStages], empty[kUpStages], a_full, a_empty, acc_full[2], acc_empty[2], mma_done;
+  uint32_t tmem;
+  int abort;
+  float red[8];
+};
+constexpr int kUpSmem = kUpA + kUpStages * kUpStage + sizeof(UpMisc);
+static_assert(kUpSmem <= 232448, "shared memory per block");
+
+__global__ void __launch_bounds__(kUpThreads, 1)
+    up_project_kernel(const __grid_constant__ CUtensorMap tmC, const __grid_constant__ CUtensorMap tmW, Params p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* const sA = smem;
+  uint8_t* const sB = smem + kUpA;
+  UpMisc& mi = *reinterpret_cast<UpMisc*>(smem + kUpA + kUpStages * kUpStage);
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const Ws& w = p.ws;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kUpStages; ++s) {
+      mbar_init(&mi.full[s], 1);
+      mbar_init(&mi.empty[s], 1);
     }
-    row0 = a.cache_offsets[lo];
-    const int64_t len = a.cache_offsets[lo + 1] - row0;
-    const int p = a.positions[t];
-    if (p >= -1 && p < len) n = p + 1;
-    else if (lane == 0) atomicOr(a.err, kErrBounds);
+    mbar_init(&mi.a_full, 1);
+    mbar_init(&mi.a_empty, 1);
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(&mi.acc_full[b], 1);
+      mbar_init(&mi.acc_empty[b], 8);
+    }
+    mbar_init(&mi.mma_done, 1);
+    mi.abort = 0;
+    fence_mbar_init();
   }
-  const uint32_t* qs = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.q) + r * 192);
-  const uint2 q0 = reinterpret_cast<const uint2*>(qs)[lane];
-  const uint32_t q1 = qs[64 + lane];
-  const float q[6] = {bf_lo(q0.x), bf_hi(q0.x), bf_lo(q0.y), bf_hi(q0.y), bf_lo(q1), bf_hi(q1)};
-  float o[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
-  for (int j = 0; j < n; ++j) {
-    const uint2* kr = reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(a.kv_exp) +
-                                                     ((row0 + j) * a.H + h) * 256);
-    const uint2 k0 = kr[lane], v = kr[32 + lane];
-    const uint32_t k1 = reinterpret_cast<const uint32_t*>(static_cast<const __nv_bfloat16*>(a.kv) +
-                                                          (row0 + j) * kLatDim + kLatV)[lane];
-    float x = q[0] * bf_lo(k0.x) + q[1] * bf_hi(k0.x) + q[2] * bf_lo(k0.y) + q[3] * bf_hi(k0.y) + q[4] * bf_lo(k1) +
-              q[5] * bf_hi(k1);
+  if (warp == 1) {
+    tmem_alloc(&mi.tmem, 512);
+    tmem_relinquish();
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  asm volatile("griddepcontrol.launch_dependents;");
+  int64_t a0, a1;
+  share(static_cast<int64_t>(w.plan->tiles) * p.H, blockIdx.x, gridDim.x, &a0, &a1);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, mi.tmem, 0);
+  const WaitCtl wc{p.err, &mi.abort, p.timeout_ns};
+  const int H = p.H;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      bool ok = true;
+      uint32_t it = 0, loads = 0;
+      for (int64_t i = a0; i < a1 && ok; ++i) {
+        const int tile = static_cast<int>(i / H), h = static_cast<int>(i % H);
+        const bool fresh = i == a0 || h == 0;
+        if (fresh) {
+          if (loads > 0 && !(ok = mbar_wait(&mi.a_empty, (loads - 1) & 1, wc))) break;
+          mbar_arrive_expect_tx(&mi.a_full, kUpA);
+          for (int c = 0; c < 8; ++c) tma_load_2d(sA + c * kChunk, &tmC, &mi.a_full, 64 * c, w.step[tile].row0);
+          ++loads;
+        }
+        for (int c = 0; c < 8; ++c, ++it) {
+          const uint32_t s = it % kUpStages;
+          if (it >= kUpStages && !(ok = mbar_wait(&mi.empty[s], (it / kUpStages - 1) & 1, wc))) break;
+          mbar_arrive_expect_tx(&mi.full[s], kUpStage);
+          tma_load_2d(sB + s * kUpStage, &tmW, &mi.full[s], 64 * c, h * 256);
+        }
+      }
+      if (!ok) {   // the loads in flight land before the block ends
+        for (uint32_t k = it > kUpStages ? it - kUpStages : 0; k < it; ++k)
+          drain(&mi.full[k % kUpStages], (k / kUpStages) & 1);
+        if (loads > 0) drain(&mi.a_full, (loads - 1) & 1);
+      }
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    const bool leader = elect_one();
+    auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity, wc)); };
+    auto commit = [&](uint64_t* bar) {
+      if (leader) umma_commit(bar);
+    };
+    constexpr uint32_t idesc = umma_idesc_bf16(128, 256);
+    const uint32_t a_lo = desc_lo(smem_u32(sA), 16), b_lo = desc_lo(smem_u32(sB), 16);
+    Ring<kUpStages> rg;
+    uint32_t nth = 0, loads = 0;
+    bool ok = true;
+    for (int64_t i = a0; i < a1 && ok; ++i, ++nth) {
+      const int h = static_cast<int>(i % H);
+      if (i == a0 || h == 0) {
+        if (!(ok = wait(&mi.a_full, loads & 1))) break;
+        ++loads;
+      }
+      const uint32_t buf = nth & 1;
+      if (nth >= 2 && !(ok = wait(&mi.acc_empty[buf], (nth / 2 - 1) & 1))) break;
+      tc_fence_after();
+#pragma unroll 1
+      for (int c = 0; c < 8; ++c) {
+        if (!(ok = wait(&mi.full[rg.s], rg.phase))) break;
+        tc_fence_after();
 #pragma unroll
-    for (int d = 16; d; d >>= 1) x += __shfl_xor_sync(0xffffffffu, x, d);
-    x *= a.scale;
-    const float mn = fmaxf(m, x);
-    const float f = m == -INFINITY ? 0.f : __expf(m - mn);
-    const float p = x == -INFINITY ? 0.f : __expf(x - mn);
-    l = l * f + p;
-    o[0] = fmaf(o[0], f, p * bf_lo(v.x));
-    o[1] = fmaf(o[1], f, p * bf_hi(v.x));
-    o[2] = fmaf(o[2], f, p * bf_lo(v.y));
-    o[3] = fmaf(o[3], f, p * bf_hi(v.y));
-    m = mn;
+        for (int k = 0; k < 4; ++k)
+          umma_lo(tmem + 256 * buf, a_lo + c * (kChunk >> 4) + 2 * k, b_lo + rg.s * (kUpStage >> 4) + 2 * k, idesc,
+                  (c | k) != 0, leader);
+        commit(&mi.empty[rg.s]);
+        rg.next();
+      }
+      if (!ok) break;
+      commit(&mi.acc_full[buf]);
+      if (h == H - 1) commit(&mi.a_empty);
+    }
+    commit(&mi.mma_done);
+    drain(&mi.mma_done, 0);
+    __syncwarp();
+  } else if (warp >= 4) {
+    // ---- epilogue: four warps for the keys, four for the values; a thread per token
+    const int part = (warp - 4) >> 2, qd = warp & 3, r = qd * 32 + lane;
+    bool ok = true;   // sticky: see expanded_kernel
+    uint32_t nth = 0;
+    uint4 rope[8];
+    int valid = 0;
+    for (int64_t i = a0; i < a1; ++i, ++nth) {
+      const int64_t tile = i / H;
+      const int h = static_cast<int>(i % H);
+      if (i == a0 || h == 0) {
+        const Steps st = w.step[tile];
+        valid = st.valid;
+        if (part == 0) {
+          const uint4* src = reinterpret_cast<const uint4*>(p.kv + (st.row0 + static_cast<int64_t>(r < valid ? r : 0)) * kLatDim + kLatV);
+#pragma unroll
+          for (int u = 0; u < 8; ++u) rope[u] = src[u];
+        }
+      }
+      const uint32_t buf = nth & 1, at = tmem + (static_cast<uint32_t>(qd * 32) << 16) + 256 * buf + 128 * part;
+      ok = ok && __all_sync(0xffffffffu, mbar_wait(&mi.acc_full[buf], (nth / 2) & 1, wc));
+      tc_fence_after();
+      float top = 0.f;
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t x[32];
+        tmem_ld_32cols(at + 32 * c, x);
+        tmem_ld_wait(x);
+#pragma unroll
+        for (int k = 0; k < 32; ++k) top = fmaxf(top, finite_abs(__uint_as_float(x[k])));
+      }
+      if (part == 0) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const uint32_t v[4] = {rope[u].x, rope[u].y, rope[u].z, rope[u].w};
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            top = fmaxf(top, fmaxf(finite_abs(__uint_as_float(v[k] << 16)), finite_abs(__uint_as_float(v[k] & 0xFFFF0000u))));
+        }
+      }
+      if (r >= valid) top = 0.f;
+      top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+      if (lane == 0) mi.red[warp - 4] = top;
+      named_bar_sync(1 + part, 128);
+      top = fmaxf(fmaxf(mi.red[4 * part], mi.red[4 * part + 1]), fmaxf(mi.red[4 * part + 2], mi.red[4 * part + 3]));
+      named_bar_sync(1 + part, 128);
+      const int f = scale_exponent(top);
+      const float inv = pow2(-f);
+      uint8_t* const dst = w.kv + (tile * H + h) * kKvBytes + part * 3 * kChunk + r * 128;
+      // 16-byte unit u of row r of a chunk lies at unit u ^ (r & 7)
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        uint32_t x[32];
+        tmem_ld_32cols(at + 32 * c, x);
+        tmem_ld_wait(x);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+          uint4 v;
+          uint32_t* const o = reinterpret_cast<uint32_t*>(&v);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            o[k] = r < valid ? pack_f16(__uint_as_float(x[8 * u + 2 * k]) * inv, __uint_as_float(x[8 * u + 2 * k + 1]) * inv) : 0u;
+          *reinterpret_cast<uint4*>(dst + (c >> 1) * kChunk + (((4 * (c & 1) + u) ^ (r & 7)) * 16)) = v;
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&mi.acc_empty[buf]);
+      if (part == 0) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const uint32_t v[4] = {rope[u].x, rope[u].y, rope[u].z, rope[u].w};
+          uint4 t;
+          uint32_t* const o = reinterpret_cast<uint32_t*>(&t);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            o[k] = r < valid ? pack_f16(__uint_as_float(v[k] << 16) * inv, __uint_as_float(v[k] & 0xFFFF0000u) * inv) : 0u;
+          *reinterpret_cast<uint4*>(dst + 2 * kChunk + ((u ^ (r & 7)) * 16)) = t;
+        }
+      }
+      if (r == 0) (part == 0 ? w.scale[tile * H + h].x : w.scale[tile * H + h].y) = static_cast<float>(f);
+    }
   }
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  const __nv_bfloat162 b0 = __floats2bfloat162_rn(o[0] * inv, o[1] * inv), b1 = __floats2bfloat162_rn(o[2] * inv, o[3] * inv);
-  reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(a.out) + r * 128)[lane] =
-      make_uint2(*reinterpret_cast<const uint32_t*>(&b0), *reinterpret_cast<const uint32_t*>(&b1));
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------- attention
+constexpr int kKStages = 4, kVStages = 2, kVStage = 2 * kChunk;
+constexpr int kQTile = 3 * kChunk;
+constexpr int kThreads = 20 * 32;
+// registers a thread: 96 at launch, then 64 (load, MMA) and 104 (softmax): 64 + 4 * 104 = 5 * 96
+constexpr int kIssueRegs = 64, kSoftRegs = 104;
+constexpr uint32_t kTmemSum = 256;             // scores of tile i at 128 i, sums at 256 + 128 i
+
+struct Misc {
+  uint64_t full_k[kKStages], empty_k[kKStages], full_v[kVStages], empty_v[kVStages];
+  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], o_free[2], mma_done;
+  uint32_t tmem;
+  int abort;
+  int item[2];                       // fetched items, in turn
+  uint64_t item_full[2], item_empty[2];
+  float red[2][2][kRowsT];           // per tile of rows, half: maxima, sums; [0] row scales at first
+};
+constexpr int kOffK = 2 * kQTile;
+constexpr int kOffV = kOffK + kKStages * kChunk;
+constexpr int kOffMisc = kOffV + kVStages * kVStage;
+constexpr int kSmem = kOffMisc + sizeof(Misc);
+static_assert(kSmem <= 232448, "shared memory per block");
+
+struct Piece {
+  Pair pr;
+  int pair, head;
+  int t0, n;            // first step, number of steps
+  bool first, last;
+};
+
+// Items in order: a group of heads, the pairs, the heads of the group.
+__device__ __forceinline__ void item_of(const Params& p, int pairs, int group, int64_t it, int* pair, int* head) {
+  const int64_t per = static_cast<int64_t>(group) * pairs;
+  const int g = static_cast<int>(it / per);
+  const int rest = static_cast<int>(it - g * per);
+  const int in = p.H - g * group < group ? p.H - g * group : group;
+  *pair = rest / in;
+  *head = g * group + rest % in;
+}
+
+// Row (t, h) of out over its own prefix, half of the dims, by one thread: for rows that a NaN or
+// an infinity beside their prefix spoiled (0 * NaN).
+__device__ __noinline__ void redo_half_row(const Params& p, int tile0, int64_t row, int head, int lim, int half) {
+  const __nv_bfloat16* const q = p.q + row * 192;
+  float m = -INFINITY, l = 0.f, o[64];
+#pragma unroll
+  for (int d = 0; d < 64; ++d) o[d] = 0.f;
+  for (int s = 0; s <= lim; ++s) {
+    const int64_t blk = static_cast<int64_t>(tile0 + s / kTok) * p.H + head;
+    const uint8_t* const kv = p.ws.kv + blk * kKvBytes;
+    const float2 sc = p.ws.scale[blk];
+    const int r = s % kTok;
+    float x = 0.f;
+    for (int d = 0; d < 192; ++d)
+      x = fmaf(__bfloat162float(q[d]),
+               __half2float(*reinterpret_cast<const __half*>(kv + (d >> 6) * kChunk + r * 128 + ((((d & 63) >> 3) ^ (r & 7)) * 16) + (d & 7) * 2)), x);
+    x *= p.scale_log2 * pow2(static_cast<int>(sc.x));
+    const float top = fmaxf(m, x), f = m == -INFINITY ? 0.f : ex2_approx(m - top);
+    const float wt = top == -INFINITY ? 0.f : ex2_approx(x - top);
+    l = fmaf(l, f, wt);
+    m = top;
+    const float vs = pow2(static_cast<int>(sc.y));
+#pragma unroll
+    for (int d = 0; d < 64; ++d) {
+      const float v = __half2float(*reinterpret_cast<const __half*>(kv + (3 + half) * kChunk + r * 128 + (((d >> 3) ^ (r & 7)) * 16) + (d & 7) * 2)) * vs;
+      o[d] = fmaf(o[d], f, wt * v);
+    }
+  }
+  const float inv = l != 0.f ? 1.f / l : 0.f;
+  uint32_t* const dst = reinterpret_cast<uint32_t*>(p.out + row * 128 + 64 * half);
+#pragma unroll
+  for (int d = 0; d < 32; ++d) dst[d] = pack2(o[2 * d] * inv, o[2 * d + 1] * inv);
+}
+
+__global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_constant__ Params p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  uint8_t* const sQ = smem;
+  uint8_t* const sK = smem + kOffK;
+  uint8_t* const sV = smem + kOffV;
+  Misc& mi = *reinterpret_cast<Misc*>(smem + kOffMisc);
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
+  const Ws& w = p.ws;
+  if (threadIdx.x == 0) {
+    for (int s = 0; s < kKStages; ++s) {
+      mbar_init(&mi.full_k[s], 1);
+      mbar_init(&mi.empty_k[s], 2);
+    }
+    for (int s = 0; s < kVStages; ++s) {
+      mbar_init(&mi.full_v[s], 1);
+      mbar_init(&mi.empty_v[s], 2);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&mi.q_full[i], 8);
+      mbar_init(&mi.s_full[i], 1);
+      mbar_init(&mi.p_full[i], 8);
+      mbar_init(&mi.o_full[i], 1);
+      mbar_init(&mi.o_free[i], 8);
+      mbar_init(&mi.item_full[i], 1);
+      mbar_init(&mi.item_empty[i], 18);   // 16 softmax and 2 MMA warps
+    }
+    mbar_init(&mi.mma_done, 2);
+    mi.abort = 0;
+    fence_mbar_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(&mi.tmem, 512);
+    tmem_relinquish();
+  }
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Plan plan = *w.plan;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (plan.bad) {
+    for (int64_t k = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x; k < static_cast<int64_t>(p.T) * p.H * 16;
+         k += static_cast<int64_t>(gridDim.x) * kThreads)
+      reinterpret_cast<uint4*>(p.out)[k] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  const uint32_t tmem = __shfl_sync(0xffffffffu, mi.tmem, 0);
+  const WaitCtl wc{p.err, &mi.abort, p.timeout_ns};
+  // heads of a group: their keys and values fit L2
+  int group = static_cast<int>(kL2Bytes / (static_cast<int64_t>(plan.tiles > 0 ? plan.tiles : 1) * kKvBytes));
+  group = group < 1 ? 1 : group > p.H ? p.H : group;
+  const int64_t items = static_cast<int64_t>(plan.pairs) * p.H, all = plan.steps * p.H;
+  int64_t at, end;                    // shares: the block's steps
+  share(all, blockIdx.x, gridDim.x, &at, &end);
+  uint32_t fetched = 0;               // items so far
+  // The next piece: of the block's share, or the next item of the counter, which warp 0 reads for
+  // all (`mine`) and hands on through a ring of two.
+  auto next = [&](Piece* pc, bool mine) {
+    if (p.split) {
+      if (at >= end) return false;
+      const int h = static_cast<int>(at / plan.steps);
+      const int64_t x = at - h * plan.steps;
+      int lo = 0, hi = plan.pairs - 1;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (w.step0[mid] <= x) lo = mid;
+        else hi = mid - 1;
+      }
+      const int64_t s0 = w.step0[lo], s1 = w.step0[lo + 1];
+      pc->pair = lo;
+      pc->head = h;
+      pc->t0 = static_cast<int>(x - s0);
+      const int64_t stop = h * plan.steps + s1 < end ? h * plan.steps + s1 : end;
+      pc->n = static_cast<int>(stop - at);
+      pc->first = x == s0;
+      pc->last = stop == h * plan.steps + s1;
+      at = stop;
+    } else {
+      const uint32_t b = fetched & 1, ph = (fetched >> 1) & 1;
+      int it;
+      if (mine) {
+        if (fetched >= 2 && !mbar_wait(&mi.item_empty[b], ph ^ 1, wc)) return false;
+        it = atomicAdd(&w.plan->next, 1);
+        if (it >= items) it = -1;
+        *reinterpret_cast<volatile int*>(&mi.item[b]) = it;
+        mbar_arrive(&mi.item_full[b]);
+      } else {
+        if (!__all_sync(0xffffffffu, mbar_wait(&mi.item_full[b], ph, wc))) return false;
+        it = *reinterpret_cast<volatile int*>(&mi.item[b]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&mi.item_empty[b]);
+      }
+      ++fetched;
+      if (it < 0) return false;
+      item_of(p, plan.pairs, group, it, &pc->pair, &pc->head);
+      pc->t0 = 0;
+      pc->n = static_cast<int>(w.step0[pc->pair + 1] - w.step0[pc->pair]);
+      pc->first = pc->last = true;
+    }
+    pc->pr = w.pair[pc->pair];
+    return true;
+  };
+  // steps of the piece that its tile i of rows takes part in
+  auto steps_of = [](const Piece& pc, int i) {
+    const int n = pc.pr.n[i] - pc.t0;
+    return n < 0 ? 0 : n < pc.n ? n : pc.n;
+  };
+  Piece pc;
+
+  if (warp < 4) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegs));
+    if (warp == 0) {
+      // ============================================================ loads
+      if (lane == 0) {
+        bool ok = true;
+        uint32_t ik = 0, iv = 0;
+        while (ok && next(&pc, true)) {
+          const int n0 = steps_of(pc, 0), n1 = steps_of(pc, 1), n = n0 > n1 ? n0 : n1;
+          for (int t = 0; t < n && ok; ++t) {
+            const uint8_t* const src =
+                w.kv + (static_cast<int64_t>(pc.pr.tile0 + pc.t0 + t) * p.H + pc.head) * kKvBytes;
+            for (int c = 0; c < 3; ++c, ++ik) {
+              const uint32_t s = ik % kKStages;
+              if (ik >= kKStages && !(ok = mbar_wait(&mi.empty_k[s], (ik / kKStages - 1) & 1, wc))) break;
+              mbar_arrive_expect_tx(&mi.full_k[s], kChunk);
+              bulk_load(sK + s * kChunk, src + c * kChunk, kChunk, &mi.full_k[s]);
+            }
+            if (!ok) break;
+            const uint32_t s = iv % kVStages;
+            if (iv >= kVStages && !(ok = mbar_wait(&mi.empty_v[s], (iv / kVStages - 1) & 1, wc))) break;
+            mbar_arrive_expect_tx(&mi.full_v[s], kVStage);
+            bulk_load(sV + s * kVStage, src + 3 * kChunk, kVStage, &mi.full_v[s]);
+            ++iv;
+          }
+        }
+        if (!ok) {   // the loads in flight land before the block ends
+          for (uint32_t k = ik > kKStages ? ik - kKStages : 0; k < ik; ++k) drain(&mi.full_k[k % kKStages], (k / kKStages) & 1);
+          for (uint32_t k = iv > kVStages ? iv - kVStages : 0; k < iv; ++k) drain(&mi.full_v[k % kVStages], (k / kVStages) & 1);
+        }
+      }
+      __syncwarp();
+    } else if (warp < 3) {
+      // ============================================================ MMAs of tile i
+      const int i = warp - 1;
+      const bool leader = elect_one();
+      auto wait = [&](uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_wait(bar, parity, wc)); };
+      auto commit = [&](uint64_t* bar) {
+        if (leader) umma_commit(bar);
+      };
+      constexpr uint32_t idesc_s = idesc_f16(128, kTok), idesc_o = idesc_f16(128, 128) | (1u << 16);   // V MN-major
+      const uint32_t q_lo = desc_lo(smem_u32(sQ + i * kQTile), 16), k_lo = desc_lo(smem_u32(sK), 16);
+      const uint32_t v_lo = desc_lo(smem_u32(sV), kChunk);
+      const uint32_t ts = tmem + 128 * i, to = tmem + kTmemSum + 128 * i;
+      Ring<kKStages> rk;
+      Ring<kVStages> rv;
+      uint32_t segs = 0, done = 0;
+      bool ok = true;
+      while (ok && next(&pc, false)) {
+        const int n = steps_of(pc, i), other = steps_of(pc, 1 - i);
+        // S = Q . K^T of the next step
+        auto scores = [&]() {
+#pragma unroll 1
+          for (int c = 0; c < 3; ++c) {
+            if (!wait(&mi.full_k[rk.s], rk.phase)) return false;
+            tc_fence_after();
+            const uint32_t a = q_lo + c * (kChunk >> 4), b = k_lo + rk.s * (kChunk >> 4);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) umma_lo(ts, a + 2 * k, b + 2 * k, idesc_s, (c | k) != 0, leader);
+            commit(&mi.empty_k[rk.s]);
+            rk.next();
+          }
+          commit(&mi.s_full[i]);
+          return true;
+        };
+        if (n > 0) {
+          if (!(ok = wait(&mi.q_full[i], segs & 1))) break;
+          tc_fence_after();
+          if (!(ok = scores())) break;
+          for (int t = 0; t < n && ok; ++t, ++done) {
+            if (!(ok = wait(&mi.p_full[i], done & 1))) break;
+            if (t == 0 && segs > 0 && !(ok = wait(&mi.o_free[i], (segs - 1) & 1))) break;
+            // O += P . V
+            if (!(ok = wait(&mi.full_v[rv.s], rv.phase))) break;
+            tc_fence_after();
+            const uint32_t b = v_lo + rv.s * (kVStage >> 4);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) umma_ta(to, ts + 8 * k, b + k * 128, idesc_o, (t | k) != 0, leader);
+            commit(&mi.empty_v[rv.s]);
+            rv.next();
+            if (t == n - 1) commit(&mi.o_full[i]);
+            else ok = scores();
+          }
+          ++segs;
+        }
+        // steps that only the other tile needs
+        for (int t = n; t < other && ok; ++t) {
+          for (int c = 0; c < 3; ++c) {
+            if (!(ok = wait(&mi.full_k[rk.s], rk.phase))) break;
+            if (leader) mbar_arrive(&mi.empty_k[rk.s]);
+            rk.next();
+          }
+          if (!ok || !(ok = wait(&mi.full_v[rv.s], rv.phase))) break;
+          if (leader) mbar_arrive(&mi.empty_v[rv.s]);
+          rv.next();
+        }
+      }
+      commit(&mi.mma_done);
+      drain(&mi.mma_done, 0);
+      __syncwarp();
+    }
+  } else {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
+    // ============================================================ softmax of tile i, half hf of the tokens
+    const int i = (warp - 4) >> 3, hf = ((warp - 4) >> 2) & 1, qd = warp & 3;
+    const int r = qd * 32 + lane;                         // row of the tile, TMEM lane
+    const uint32_t tlane = tmem + (static_cast<uint32_t>(qd * 32) << 16);
+    const uint32_t ts = tlane + 128 * i, to = tlane + kTmemSum + 128 * i + 64 * hf;
+    const int bar = 1 + i;
+    uint32_t done = 0, segs = 0;
+    // A wait that ran out is skipped from then on, but a piece is walked to its end: the warps of a
+    // tile meet at named barriers.  The results are then worthless, and the error word says so.
+    bool ok = true;
+    while (!named_bar_or(bar, 256, !next(&pc, false))) {   // all the tile's warps have a piece, or all leave
+      const int n = steps_of(pc, i);
+      const int tok = i * kRowsT + r;                     // query of the pair
+      const bool real = tok < pc.pr.ntok;
+      const int64_t row = static_cast<int64_t>(pc.pr.tok0 + tok) * p.H + pc.head;
+      int lim = -1;
+      if (real) {
+        lim = p.positions[pc.pr.tok0 + tok];
+        if (lim < -1 || lim >= pc.pr.seq_len) lim = -1;
+      }
+      float a = 0.f;
+      if (n > 0) {
+        // Q in fp16, a row at a time: lane l holds values 2l, 2l + 1 of each 64; 16 rows a warp
+        const int w8 = (warp - 4) & 7;
+        const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q);
+#pragma unroll 1
+        for (int k0 = 0; k0 < 16; k0 += 4) {
+          uint32_t v[4][3];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int j = i * kRowsT + w8 * 16 + k0 + k;
+            const bool have = j < pc.pr.ntok;
+            const uint32_t* const q = src + (static_cast<int64_t>(pc.pr.tok0 + (have ? j : 0)) * p.H + pc.head) * 96;
+#pragma unroll
+            for (int c = 0; c < 3; ++c) v[k][c] = have ? q[32 * c + lane] : 0u;
+          }
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const int rr = w8 * 16 + k0 + k;
+            float top = 0.f;
+#pragma unroll
+            for (int c = 0; c < 3; ++c)
+              top = fmaxf(top, fmaxf(finite_abs(__uint_as_float(v[k][c] << 16)), finite_abs(__uint_as_float(v[k][c] & 0xFFFF0000u))));
+            top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+            const int f = scale_exponent(top);
+            const float inv = pow2(-f);
+#pragma unroll
+            for (int c = 0; c < 3; ++c)
+              *reinterpret_cast<uint32_t*>(sQ + i * kQTile + c * kChunk + rr * 128 + (((lane >> 2) ^ (rr & 7)) * 16) + (lane & 3) * 4) =
+                  pack_f16(__uint_as_float(v[k][c] << 16) * inv, __uint_as_float(v[k][c] & 0xFFFF0000u) * inv);
+            if (lane == 0) mi.red[i][0][rr] = pow2(f);
+          }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&mi.q_full[i]);
+        named_bar_sync(bar, 256);
+        a = p.scale_log2 * mi.red[i][0][r];
+        named_bar_sync(bar, 256);
+      }
+      const int low = __reduce_min_sync(0xffffffffu, real ? lim : 0x7FFFFFFF);   // of the warp's rows
+      float m = kUnset, l = 0.f;
+      const float2* const scales = w.scale + static_cast<int64_t>(pc.pr.tile0 + pc.t0) * p.H + pc.head;
+      float2 sc = make_float2(0.f, 0.f);
+      if (n > 0) sc = scales[0];
+#pragma unroll 1
+      for (int t = 0; t < n; ++t, ++done) {
+        const float ak = a * pow2(static_cast<int>(sc.x)), fv = sc.y;
+        if (t + 1 < n) sc = scales[static_cast<int64_t>(t + 1) * p.H];
+        const int pos0 = (pc.t0 + t) * kTok + 64 * hf;
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(&mi.s_full[i], done & 1, wc));
+        tc_fence_after();
+        uint32_t x[2][32];
+        tmem_ld_32cols(ts + 64 * hf, x[0]);
+        tmem_ld_32cols(ts + 64 * hf + 32, x[1]);
+        tmem_ld_wait(x[0]);
+        tmem_ld_wait(x[1]);
+        if (pos0 + 63 > low) {
+          const int rel = lim - pos0;
+#pragma unroll
+          for (int c = 0; c < 64; ++c)
+            if (c > rel) x[c >> 5][c & 31] = 0xFF800000u;
+        }
+        float top = -INFINITY;
+#pragma unroll
+        for (int c = 0; c < 64; c += 2)
+          top = fmaxf(top, fmaxf(__uint_as_float(x[c >> 5][c & 31]), __uint_as_float(x[c >> 5][(c & 31) + 1])));
+        top = fmaf(top, ak, fv);
+        tc_fence_before();
+        if (named_bar_or(bar, 256, top > m + 8.f)) {
+          // some row's reference rises: the maximum of both halves of its tokens
+          mi.red[i][hf][r] = top;
+          named_bar_sync(bar, 256);
+          top = fmaxf(mi.red[i][0][r], mi.red[i][1][r]);
+          const float now = top > m + 8.f ? top : m;
+          const float f = ex2_approx(m - now);
+          m = now;
+          l *= f;
+          tc_fence_after();
+          if (t > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+            // the sums so far (the scores' barrier covers the products before them)
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              float o[16];
+              tmem_ld16(to + 16 * c, o);
+#pragma unroll
+              for (int k = 0; k < 16; ++k) o[k] *= f;
+              tmem_st16(to + 16 * c, o);
+            }
+          }
+          named_bar_sync(bar, 256);     // red is free again
+        }
+        tc_fence_after();               // both halves have taken their scores: weights may replace them
+        const float2 a2 = make_float2(ak, ak), c2 = make_float2(fv + kLift - m, fv + kLift - m);
+        float2 sum = make_float2(0.f, 0.f);
+        uint32_t pk[32];
+#pragma unroll
+        for (int c = 0; c < 32; ++c) {
+          const float2 y = ffma2(make_float2(__uint_as_float(x[c >> 4][2 * (c & 15)]), __uint_as_float(x[c >> 4][2 * (c & 15) + 1])), a2, c2);
+          const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+          sum = __fadd2_rn(sum, e);
+          pk[c] = pack_f16(e.x, e.y);
+        }
+        asm volatile(
+            "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+            "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+            "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};\n\t"
+            "tcgen05.wait::st.sync.aligned;" ::"r"(ts + 32 * hf),
+            "r"(pk[0]), "r"(pk[1]), "r"(pk[2]), "r"(pk[3]), "r"(pk[4]), "r"(pk[5]), "r"(pk[6]), "r"(pk[7]), "r"(pk[8]),
+            "r"(pk[9]), "r"(pk[10]), "r"(pk[11]), "r"(pk[12]), "r"(pk[13]), "r"(pk[14]), "r"(pk[15]), "r"(pk[16]),
+            "r"(pk[17]), "r"(pk[18]), "r"(pk[19]), "r"(pk[20]), "r"(pk[21]), "r"(pk[22]), "r"(pk[23]), "r"(pk[24]),
+            "r"(pk[25]), "r"(pk[26]), "r"(pk[27]), "r"(pk[28]), "r"(pk[29]), "r"(pk[30]), "r"(pk[31])
+            : "memory");
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&mi.p_full[i]);
+        l = fmaf(sum.x + sum.y, pow2(-static_cast<int>(fv)), l);
+      }
+      if (n > 0) {
+        mi.red[i][hf][r] = l;
+        named_bar_sync(bar, 256);
+        l = mi.red[i][0][r] + mi.red[i][1][r];
+        ok = ok && __all_sync(0xffffffffu, mbar_wait(&mi.o_full[i], segs & 1, wc));
+        tc_fence_after();
+        ++segs;
+      }
+      const bool whole = pc.first && pc.last;
+      const float inv = l != 0.f ? 1.f / l : 0.f;
+      const int64_t slot = 2 * blockIdx.x + (pc.first ? 1 : 0);    // head pieces 0, tail pieces 1
+      bool nan = false;
+#pragma unroll 1
+      for (int c = 0; c < 4; ++c) {
+        float o[16];
+        if (n > 0) tmem_ld16(to + 16 * c, o);
+        if (real && whole) {
+          uint32_t v[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const float v0 = l != 0.f ? o[2 * k] * inv : 0.f, v1 = l != 0.f ? o[2 * k + 1] * inv : 0.f;
+            nan |= v0 != v0 || v1 != v1;
+            v[k] = pack2(v0, v1);
+          }
+          uint4* const dst = reinterpret_cast<uint4*>(p.out + row * 128 + 64 * hf + 16 * c);
+          dst[0] = make_uint4(v[0], v[1], v[2], v[3]);
+          dst[1] = make_uint4(v[4], v[5], v[6], v[7]);
+        } else if (real && n > 0) {
+          float4* const dst = reinterpret_cast<float4*>(w.o + (slot * kPair + tok) * 128 + 64 * hf + 16 * c);
+#pragma unroll
+          for (int k = 0; k < 4; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        }
+        __syncwarp();
+      }
+      if (!whole && hf == 0) w.ml[slot * kPair + tok] = make_float2(m, n > 0 ? l : 0.f);
+      if (n > 0) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&mi.o_free[i]);
+      }
+      if (nan && inv == inv) redo_half_row(p, pc.pr.tile0, row, pc.head, lim, hf);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------- merge (shares)
+// A row of an item from its pieces, in the order of their steps; a warp per row.
+constexpr int kMergeThreads = 128;
+
+__global__ void __launch_bounds__(kMergeThreads) merge_expanded_kernel(const __grid_constant__ Params p, int blocks) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const Ws& w = p.ws;
+  const Plan plan = *w.plan;
+  const int lane = threadIdx.x & 31;
+  const int64_t all = plan.steps * p.H;
+  for (int item = blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5); item < plan.merges * kPair;
+       item += gridDim.x * (kMergeThreads / 32)) {
+    const Merge mg = w.merge[item / kPair];
+    const Pair pr = w.pair[mg.pair];
+    const int tok = item % kPair;
+    if (tok >= pr.ntok) continue;
+    float m = kUnset;
+    for (int k = mg.first; k <= mg.last; ++k) {
+      int64_t x, y;
+      share(all, k, blocks, &x, &y);
+      if (x >= y) continue;
+      const float2 v = w.ml[static_cast<int64_t>(2 * k + (k == mg.first)) * kPair + tok];
+      if (v.y != 0.f) m = fmaxf(m, v.x);
+    }
+    float l = 0.f;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = mg.first; k <= mg.last; ++k) {
+      int64_t x, y;
+      share(all, k, blocks, &x, &y);
+      if (x >= y) continue;
+      const int64_t at = static_cast<int64_t>(2 * k + (k == mg.first)) * kPair + tok;
+      const float2 v = w.ml[at];
+      if (v.y == 0.f) continue;
+      const float4 c = reinterpret_cast<const float4*>(w.o + at * 128)[lane];
+      const float f = ex2_approx(v.x - m);
+      l = fmaf(v.y, f, l);
+      o.x = fmaf(c.x, f, o.x);
+      o.y = fmaf(c.y, f, o.y);
+      o.z = fmaf(c.z, f, o.z);
+      o.w = fmaf(c.w, f, o.w);
+    }
+    const float inv = l != 0.f ? 1.f / l : 0.f;
+    const int64_t row = static_cast<int64_t>(pr.tok0 + tok) * p.H + mg.head;
+    reinterpret_cast<uint2*>(p.out + row * 128)[lane] =
+        l != 0.f ? make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv)) : make_uint2(0u, 0u);
+    const bool nan = inv == inv && !(o.x == o.x && o.y == o.y && o.z == o.z && o.w == o.w);
+    if (__any_sync(0xffffffffu, nan) && lane < 2) redo_half_row(p, pr.tile0, row, mg.head, p.positions[pr.tok0 + tok], lane);
+  }
 }
 
 }  // namespace
 
-int64_t expanded_plan_bytes(int64_t, int64_t, int64_t, int) { return 16; }
+int64_t expanded_workspace_bytes(int64_t T, int64_t B, int64_t H, int64_t cache_rows, int num_sms) {
+  return carve(nullptr, T, B, H, cache_rows, num_sms).bytes;
+}
 
-cudaError_t launch_latent_expanded(const ExpandedArgs& a, cudaStream_t s) {
+cudaError_t launch_latent_expanded(const ExpandedArgs& a, const CUtensorMap& tmC, const CUtensorMap& tmW, cudaStream_t s) {
   if (a.T == 0) return cudaSuccess;
-  int* bad = static_cast<int*>(a.plan);
-  check_offsets_kernel<<<1, 256, 0, s>>>(a, bad);
-  const int64_t rows = static_cast<int64_t>(a.T) * a.H;
-  expanded_simple_kernel<<<static_cast<unsigned>((rows + kWarps - 1) / kWarps), kWarps * 32, 0, s>>>(a, bad);
-  return cudaGetLastError();
+  const int blocks = a.num_sms;
+  Params p;
+  p.T = a.T;
+  p.B = a.B;
+  p.H = a.H;
+  p.cache_rows = a.cache_rows;
+  p.q = static_cast<const __nv_bfloat16*>(a.q);
+  p.kv = static_cast<const __nv_bfloat16*>(a.kv);
+  p.positions = a.positions;
+  p.q_seq_offsets = a.q_seq_offsets;
+  p.cache_offsets = a.cache_offsets;
+  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.out = static_cast<__nv_bfloat16*>(a.out);
+  p.ws = carve(a.workspace, a.T, a.B, a.H, a.cache_rows, blocks);
+  p.err = a.err;
+  p.timeout_ns = a.timeout_ns;
+  // fewer than six items a block would leave blocks idle at the end
+  p.split = (static_cast<int64_t>(a.T) + kPair - 1) / kPair * a.H < 6 * blocks;
+  cudaError_t e = cudaFuncSetAttribute(up_project_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kUpSmem);
+  if (e == cudaSuccess) e = cudaFuncSetAttribute(expanded_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  if (e != cudaSuccess) return e;
+  expanded_plan_kernel<<<1, kPlanThreads, 0, s>>>(p, blocks);
+  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  // the later kernels start while their predecessor runs out and wait for its results themselves
+  cudaLaunchAttribute dep;
+  dep.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  dep.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(blocks);
+  cfg.blockDim = dim3(kUpThreads);
+  cfg.dynamicSmemBytes = kUpSmem;
+  cfg.stream = s;
+  cfg.attrs = &dep;
+  cfg.numAttrs = 1;
+  if ((e = cudaLaunchKernelEx(&cfg, up_project_kernel, tmC, tmW, p)) != cudaSuccess) return e;
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmem;
+  if ((e = cudaLaunchKernelEx(&cfg, expanded_kernel, p)) != cudaSuccess) return e;
+  if (!p.split) return cudaSuccess;
+  cfg.gridDim = dim3(8 * blocks);
+  cfg.blockDim = dim3(kMergeThreads);
+  cfg.dynamicSmemBytes = 0;
+  return cudaLaunchKernelEx(&cfg, merge_expanded_kernel, p, blocks);
 }
 
 }  // namespace dsa
