@@ -17,11 +17,11 @@
 //   them with plain bulk copies.  One block per SM, the tokens' latents stay in shared memory
 //   for all heads, W streams through a ring, and the epilogue of a head (8 warps) runs under
 //   the MMAs of the next (two accumulators of 256 TMEM columns).
-// expanded_kernel: one block of 20 warps per SM.  An item is (256 queries, head): two tiles of
+// expanded_kernel: one block of 12 warps per SM.  An item is (256 queries, head): two tiles of
 //   128 rows, whose scores (128 columns each) and sums (128) fill TMEM.  One warp issues the MMAs
 //   of a tile, so that the tensor core works on one tile while the softmax of the other runs;
-//   two warpgroups do that softmax, a thread for half of a row (64 tokens).  The weights
-//   replace the scores in TMEM (the A operand of the second product).  K and V of 128 tokens
+//   four warps do that softmax, a thread per row, so that no warp waits for another one.  The
+//   weights replace the scores in TMEM (the A operand of the second product).  K and V of 128 tokens
 //   are 80 KB, read once for both tiles, through rings of four 16 KB and two 32 KB stages.
 //   Items are taken in order from a counter, longest first among a sequence's; the heads go in
 //   groups whose keys and values fit L2.  When there are too few items for that to balance,
@@ -425,7 +425,7 @@ __global__ void __launch_bounds__(kUpThreads, 1)
   } else if (warp >= 4) {
     // ---- epilogue: four warps for the keys, four for the values; a thread per token
     const int part = (warp - 4) >> 2, qd = warp & 3, r = qd * 32 + lane;
-    bool ok = true;   // sticky: see expanded_kernel
+    bool ok = true;   // a wait that ran out is skipped from then on: the warps of a part meet at named barriers
     uint32_t nth = 0;
     uint4 rope[8];
     int valid = 0;
@@ -516,19 +516,20 @@ __global__ void __launch_bounds__(kUpThreads, 1)
 // ---------------------------------------------------------------- attention
 constexpr int kKStages = 4, kVStages = 2, kVStage = 2 * kChunk;
 constexpr int kQTile = 3 * kChunk;
-constexpr int kThreads = 20 * 32;
-// registers a thread: 96 at launch, then 64 (load, MMA) and 104 (softmax): 64 + 4 * 104 = 5 * 96
-constexpr int kIssueRegs = 64, kSoftRegs = 104;
+constexpr int kThreads = 12 * 32;
+// registers a thread: 168 at launch, then 88 (load, MMA) and 208 (softmax): 88 + 2 * 208 = 3 * 168
+constexpr int kIssueRegs = 88, kSoftRegs = 208;
+constexpr uint64_t kTurnNs = 20000;            // longest wait for the other tile's turn
 constexpr uint32_t kTmemSum = 256;             // scores of tile i at 128 i, sums at 256 + 128 i
 
 struct Misc {
   uint64_t full_k[kKStages], empty_k[kKStages], full_v[kVStages], empty_v[kVStages];
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], o_free[2], mma_done;
+  uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2], o_free[2], mma_done;
   uint32_t tmem;
   int abort;
   int item[2];                       // fetched items, in turn
   uint64_t item_full[2], item_empty[2];
-  float red[2][2][kRowsT];           // per tile of rows, half: maxima, sums; [0] row scales at first
+  uint32_t turns[2];                 // softmax warps of a tile that are past their exponentials, in all
 };
 constexpr int kOffK = 2 * kQTile;
 constexpr int kOffV = kOffK + kKStages * kChunk;
@@ -605,13 +606,15 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
       mbar_init(&mi.empty_v[s], 2);
     }
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&mi.q_full[i], 8);
+      mbar_init(&mi.q_full[i], 4);
       mbar_init(&mi.s_full[i], 1);
-      mbar_init(&mi.p_full[i], 8);
+      mbar_init(&mi.p_full[i][0], 4);
+      mbar_init(&mi.p_full[i][1], 4);
       mbar_init(&mi.o_full[i], 1);
-      mbar_init(&mi.o_free[i], 8);
+      mbar_init(&mi.o_free[i], 4);
       mbar_init(&mi.item_full[i], 1);
-      mbar_init(&mi.item_empty[i], 18);   // 16 softmax and 2 MMA warps
+      mbar_init(&mi.item_empty[i], 10);   // 8 softmax and 2 MMA warps
+      mi.turns[i] = 0;
     }
     mbar_init(&mi.mma_done, 2);
     mi.abort = 0;
@@ -764,14 +767,18 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
           tc_fence_after();
           if (!(ok = scores())) break;
           for (int t = 0; t < n && ok; ++t, ++done) {
-            if (!(ok = wait(&mi.p_full[i], done & 1))) break;
+            if (!(ok = wait(&mi.p_full[i][0], done & 1))) break;
             if (t == 0 && segs > 0 && !(ok = wait(&mi.o_free[i], (segs - 1) & 1))) break;
-            // O += P . V
+            // O += P . V, half of the tokens as soon as their weights are there
             if (!(ok = wait(&mi.full_v[rv.s], rv.phase))) break;
             tc_fence_after();
             const uint32_t b = v_lo + rv.s * (kVStage >> 4);
 #pragma unroll
-            for (int k = 0; k < 8; ++k) umma_ta(to, ts + 8 * k, b + k * 128, idesc_o, (t | k) != 0, leader);
+            for (int k = 0; k < 4; ++k) umma_ta(to, ts + 8 * k, b + k * 128, idesc_o, (t | k) != 0, leader);
+            if (!(ok = wait(&mi.p_full[i][1], done & 1))) break;
+            tc_fence_after();
+#pragma unroll
+            for (int k = 4; k < 8; ++k) umma_ta(to, ts + 8 * k, b + k * 128, idesc_o, true, leader);
             commit(&mi.empty_v[rv.s]);
             rv.next();
             if (t == n - 1) commit(&mi.o_full[i]);
@@ -797,18 +804,15 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
     }
   } else {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kSoftRegs));
-    // ============================================================ softmax of tile i, half hf of the tokens
-    const int i = (warp - 4) >> 3, hf = ((warp - 4) >> 2) & 1, qd = warp & 3;
+    // ============================================================ softmax of tile i, a thread per row
+    const int i = (warp - 4) >> 2, qd = warp & 3;
     const int r = qd * 32 + lane;                         // row of the tile, TMEM lane
     const uint32_t tlane = tmem + (static_cast<uint32_t>(qd * 32) << 16);
-    const uint32_t ts = tlane + 128 * i, to = tlane + kTmemSum + 128 * i + 64 * hf;
-    const int bar = 1 + i;
-    uint32_t done = 0, segs = 0;
-    // A wait that ran out is skipped from then on, but a piece is walked to its end: the warps of a
-    // tile meet at named barriers.  The results are then worthless, and the error word says so.
+    const uint32_t ts = tlane + 128 * i, to = tlane + kTmemSum + 128 * i;
+    uint32_t done = 0, segs = 0, theirs = 0;              // steps of this tile, pieces, steps of the other
     bool ok = true;
-    while (!named_bar_or(bar, 256, !next(&pc, false))) {   // all the tile's warps have a piece, or all leave
-      const int n = steps_of(pc, i);
+    while (ok && next(&pc, false)) {
+      const int n = steps_of(pc, i), other = steps_of(pc, 1 - i);
       const int tok = i * kRowsT + r;                     // query of the pair
       const bool real = tok < pc.pr.ntok;
       const int64_t row = static_cast<int64_t>(pc.pr.tok0 + tok) * p.H + pc.head;
@@ -819,23 +823,22 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
       }
       float a = 0.f;
       if (n > 0) {
-        // Q in fp16, a row at a time: lane l holds values 2l, 2l + 1 of each 64; 16 rows a warp
-        const int w8 = (warp - 4) & 7;
-        const uint32_t* src = reinterpret_cast<const uint32_t*>(p.q);
+        // the warp's 32 rows of Q in fp16: lane l holds values 2l, 2l + 1 of each 64 of a row
+        const uint32_t* const src = reinterpret_cast<const uint32_t*>(p.q);
 #pragma unroll 1
-        for (int k0 = 0; k0 < 16; k0 += 4) {
-          uint32_t v[4][3];
+        for (int k0 = 0; k0 < 32; k0 += 8) {
+          uint32_t v[8][3];
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int j = i * kRowsT + w8 * 16 + k0 + k;
+          for (int k = 0; k < 8; ++k) {
+            const int j = i * kRowsT + qd * 32 + k0 + k;
             const bool have = j < pc.pr.ntok;
             const uint32_t* const q = src + (static_cast<int64_t>(pc.pr.tok0 + (have ? j : 0)) * p.H + pc.head) * 96;
 #pragma unroll
             for (int c = 0; c < 3; ++c) v[k][c] = have ? q[32 * c + lane] : 0u;
           }
 #pragma unroll
-          for (int k = 0; k < 4; ++k) {
-            const int rr = w8 * 16 + k0 + k;
+          for (int k = 0; k < 8; ++k) {
+            const int rr = qd * 32 + k0 + k;
             float top = 0.f;
 #pragma unroll
             for (int c = 0; c < 3; ++c)
@@ -847,15 +850,12 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
             for (int c = 0; c < 3; ++c)
               *reinterpret_cast<uint32_t*>(sQ + i * kQTile + c * kChunk + rr * 128 + (((lane >> 2) ^ (rr & 7)) * 16) + (lane & 3) * 4) =
                   pack_f16(__uint_as_float(v[k][c] << 16) * inv, __uint_as_float(v[k][c] & 0xFFFF0000u) * inv);
-            if (lane == 0) mi.red[i][0][rr] = pow2(f);
+            if (lane == k0 + k) a = p.scale_log2 * pow2(f);
           }
         }
         fence_proxy_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&mi.q_full[i]);
-        named_bar_sync(bar, 256);
-        a = p.scale_log2 * mi.red[i][0][r];
-        named_bar_sync(bar, 256);
       }
       const int low = __reduce_min_sync(0xffffffffu, real ? lim : 0x7FFFFFFF);   // of the warp's rows
       float m = kUnset, l = 0.f;
@@ -866,40 +866,37 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
       for (int t = 0; t < n; ++t, ++done) {
         const float ak = a * pow2(static_cast<int>(sc.x)), fv = sc.y;
         if (t + 1 < n) sc = scales[static_cast<int64_t>(t + 1) * p.H];
-        const int pos0 = (pc.t0 + t) * kTok + 64 * hf;
+        const int pos0 = (pc.t0 + t) * kTok;
         ok = ok && __all_sync(0xffffffffu, mbar_wait(&mi.s_full[i], done & 1, wc));
         tc_fence_after();
-        uint32_t x[2][32];
-        tmem_ld_32cols(ts + 64 * hf, x[0]);
-        tmem_ld_32cols(ts + 64 * hf + 32, x[1]);
-        tmem_ld_wait(x[0]);
-        tmem_ld_wait(x[1]);
-        if (pos0 + 63 > low) {
+        uint32_t x[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_32cols(ts + 32 * c, x[c]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_wait(x[c]);
+        if (pos0 + kTok - 1 > low) {
           const int rel = lim - pos0;
 #pragma unroll
-          for (int c = 0; c < 64; ++c)
+          for (int c = 0; c < kTok; ++c)
             if (c > rel) x[c >> 5][c & 31] = 0xFF800000u;
         }
-        float top = -INFINITY;
+        float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-        for (int c = 0; c < 64; c += 2)
-          top = fmaxf(top, fmaxf(__uint_as_float(x[c >> 5][c & 31]), __uint_as_float(x[c >> 5][(c & 31) + 1])));
-        top = fmaf(top, ak, fv);
-        tc_fence_before();
-        if (named_bar_or(bar, 256, top > m + 8.f)) {
-          // some row's reference rises: the maximum of both halves of its tokens
-          mi.red[i][hf][r] = top;
-          named_bar_sync(bar, 256);
-          top = fmaxf(mi.red[i][0][r], mi.red[i][1][r]);
+        for (int c = 0; c < 32; c += 2)
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            tops[k] = fmaxf(tops[k], fmaxf(__uint_as_float(x[k][c]), __uint_as_float(x[k][c + 1])));
+        const float top = fmaf(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])), ak, fv);
+        if (__any_sync(0xffffffffu, top > m + 8.f)) {
+          // some row's reference rises
           const float now = top > m + 8.f ? top : m;
           const float f = ex2_approx(m - now);
           m = now;
           l *= f;
-          tc_fence_after();
-          if (t > 0 && __any_sync(0xffffffffu, f != 1.f)) {
+          if (t > 0) {
             // the sums so far (the scores' barrier covers the products before them)
 #pragma unroll 1
-            for (int c = 0; c < 4; ++c) {
+            for (int c = 0; c < 8; ++c) {
               float o[16];
               tmem_ld16(to + 16 * c, o);
 #pragma unroll
@@ -907,38 +904,53 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
               tmem_st16(to + 16 * c, o);
             }
           }
-          named_bar_sync(bar, 256);     // red is free again
         }
-        tc_fence_after();               // both halves have taken their scores: weights may replace them
+        // The exponentials of the two tiles alternate, 0 before 1 in every step; left alone the tiles
+        // fall into step, both softmaxes then wait for both products and a step takes twice as long.
+        // Nothing depends on the order, so the wait is short and gives up without an error.
+        {
+          const uint32_t before = 4 * (theirs + (t + i < other ? t + i : other));
+          const volatile uint32_t* const turns = &mi.turns[1 - i];
+          if (static_cast<int32_t>(*turns - before) < 0) {
+            const uint64_t t0 = global_timer_ns();
+            while (static_cast<int32_t>(*turns - before) < 0 && global_timer_ns() - t0 < kTurnNs) {
+            }
+          }
+          __syncwarp();
+        }
         const float2 a2 = make_float2(ak, ak), c2 = make_float2(fv + kLift - m, fv + kLift - m);
-        float2 sum = make_float2(0.f, 0.f);
-        uint32_t pk[32];
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-        for (int c = 0; c < 32; ++c) {
-          const float2 y = ffma2(make_float2(__uint_as_float(x[c >> 4][2 * (c & 15)]), __uint_as_float(x[c >> 4][2 * (c & 15) + 1])), a2, c2);
-          const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
-          sum = __fadd2_rn(sum, e);
-          pk[c] = pack_f16(e.x, e.y);
+        for (int hf = 0; hf < 2; ++hf) {
+          uint32_t pk[32];
+#pragma unroll
+          for (int c = 0; c < 32; ++c) {
+            const int k = 2 * hf + (c >> 4), j = 2 * (c & 15);
+            const float2 y = ffma2(make_float2(__uint_as_float(x[k][j]), __uint_as_float(x[k][j + 1])), a2, c2);
+            const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
+            sum[c & 1] = __fadd2_rn(sum[c & 1], e);
+            pk[c] = pack_f16(e.x, e.y);
+          }
+          if (hf == 1 && lane == 0) atomicAdd(&mi.turns[i], 1u);
+          asm volatile(
+              "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+              "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
+              "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};\n\t"
+              "tcgen05.wait::st.sync.aligned;" ::"r"(ts + 32 * hf),
+              "r"(pk[0]), "r"(pk[1]), "r"(pk[2]), "r"(pk[3]), "r"(pk[4]), "r"(pk[5]), "r"(pk[6]), "r"(pk[7]),
+              "r"(pk[8]), "r"(pk[9]), "r"(pk[10]), "r"(pk[11]), "r"(pk[12]), "r"(pk[13]), "r"(pk[14]), "r"(pk[15]),
+              "r"(pk[16]), "r"(pk[17]), "r"(pk[18]), "r"(pk[19]), "r"(pk[20]), "r"(pk[21]), "r"(pk[22]), "r"(pk[23]),
+              "r"(pk[24]), "r"(pk[25]), "r"(pk[26]), "r"(pk[27]), "r"(pk[28]), "r"(pk[29]), "r"(pk[30]), "r"(pk[31])
+              : "memory");
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&mi.p_full[i][hf]);
         }
-        asm volatile(
-            "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-            "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, "
-            "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32};\n\t"
-            "tcgen05.wait::st.sync.aligned;" ::"r"(ts + 32 * hf),
-            "r"(pk[0]), "r"(pk[1]), "r"(pk[2]), "r"(pk[3]), "r"(pk[4]), "r"(pk[5]), "r"(pk[6]), "r"(pk[7]), "r"(pk[8]),
-            "r"(pk[9]), "r"(pk[10]), "r"(pk[11]), "r"(pk[12]), "r"(pk[13]), "r"(pk[14]), "r"(pk[15]), "r"(pk[16]),
-            "r"(pk[17]), "r"(pk[18]), "r"(pk[19]), "r"(pk[20]), "r"(pk[21]), "r"(pk[22]), "r"(pk[23]), "r"(pk[24]),
-            "r"(pk[25]), "r"(pk[26]), "r"(pk[27]), "r"(pk[28]), "r"(pk[29]), "r"(pk[30]), "r"(pk[31])
-            : "memory");
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&mi.p_full[i]);
-        l = fmaf(sum.x + sum.y, pow2(-static_cast<int>(fv)), l);
+        sum[0] = __fadd2_rn(sum[0], sum[1]);
+        l = fmaf(sum[0].x + sum[0].y, pow2(-static_cast<int>(fv)), l);
       }
+      theirs += other;
       if (n > 0) {
-        mi.red[i][hf][r] = l;
-        named_bar_sync(bar, 256);
-        l = mi.red[i][0][r] + mi.red[i][1][r];
         ok = ok && __all_sync(0xffffffffu, mbar_wait(&mi.o_full[i], segs & 1, wc));
         tc_fence_after();
         ++segs;
@@ -948,7 +960,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
       const int64_t slot = 2 * blockIdx.x + (pc.first ? 1 : 0);    // head pieces 0, tail pieces 1
       bool nan = false;
 #pragma unroll 1
-      for (int c = 0; c < 4; ++c) {
+      for (int c = 0; c < 8; ++c) {
         float o[16];
         if (n > 0) tmem_ld16(to + 16 * c, o);
         if (real && whole) {
@@ -959,23 +971,27 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
             nan |= v0 != v0 || v1 != v1;
             v[k] = pack2(v0, v1);
           }
-          uint4* const dst = reinterpret_cast<uint4*>(p.out + row * 128 + 64 * hf + 16 * c);
+          uint4* const dst = reinterpret_cast<uint4*>(p.out + row * 128 + 16 * c);
           dst[0] = make_uint4(v[0], v[1], v[2], v[3]);
           dst[1] = make_uint4(v[4], v[5], v[6], v[7]);
         } else if (real && n > 0) {
-          float4* const dst = reinterpret_cast<float4*>(w.o + (slot * kPair + tok) * 128 + 64 * hf + 16 * c);
+          float4* const dst = reinterpret_cast<float4*>(w.o + (slot * kPair + tok) * 128 + 16 * c);
 #pragma unroll
           for (int k = 0; k < 4; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
         }
         __syncwarp();
       }
-      if (!whole && hf == 0) w.ml[slot * kPair + tok] = make_float2(m, n > 0 ? l : 0.f);
+      if (!whole) w.ml[slot * kPair + tok] = make_float2(m, l);
       if (n > 0) {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&mi.o_free[i]);
       }
-      if (nan && inv == inv) redo_half_row(p, pc.pr.tile0, row, pc.head, lim, hf);
+      if (nan && inv == inv) {
+        redo_half_row(p, pc.pr.tile0, row, pc.head, lim, 0);
+        redo_half_row(p, pc.pr.tile0, row, pc.head, lim, 1);
+      }
+      __syncwarp();
     }
   }
   tc_fence_before();
