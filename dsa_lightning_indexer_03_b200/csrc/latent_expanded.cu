@@ -299,6 +299,18 @@ __device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t b
                : "memory");
 }
 
+// 32 bytes, a whole sector, to a 32-byte aligned address
+__device__ __forceinline__ void store32(void* p, uint4 a, uint4 b) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w),
+               "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
+// 16-byte units u, u + 1 (u even) of row r of a chunk: they lie at units u ^ (r & 7), (u + 1) ^ (r & 7),
+// in the same 32 bytes
+__device__ __forceinline__ void store_units(uint8_t* row, int r, int u, uint4 a, uint4 b) {
+  store32(row + ((u ^ (r & 6)) * 16), r & 1 ? b : a, r & 1 ? a : b);
+}
+
 __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
   const uint64_t t0 = global_timer_ns();
   while (!mbar_try_wait(smem_u32(bar), parity) && global_timer_ns() - t0 <= kDrainNs) {
@@ -471,35 +483,32 @@ __global__ void __launch_bounds__(kUpThreads, 1)
       const int f = scale_exponent(top);
       const float inv = pow2(-f);
       uint8_t* const dst = w.kv + (tile * H + h) * kKvBytes + part * 3 * kChunk + r * 128;
-      // 16-byte unit u of row r of a chunk lies at unit u ^ (r & 7)
 #pragma unroll 1
       for (int c = 0; c < 4; ++c) {
         uint32_t x[32];
         tmem_ld_32cols(at + 32 * c, x);
         tmem_ld_wait(x);
+        uint4 v[4];
+        uint32_t* const o = reinterpret_cast<uint32_t*>(v);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          uint4 v;
-          uint32_t* const o = reinterpret_cast<uint32_t*>(&v);
-#pragma unroll
-          for (int k = 0; k < 4; ++k)
-            o[k] = r < valid ? pack_f16(__uint_as_float(x[8 * u + 2 * k]) * inv, __uint_as_float(x[8 * u + 2 * k + 1]) * inv) : 0u;
-          *reinterpret_cast<uint4*>(dst + (c >> 1) * kChunk + (((4 * (c & 1) + u) ^ (r & 7)) * 16)) = v;
-        }
+        for (int k = 0; k < 16; ++k)
+          o[k] = r < valid ? pack_f16(__uint_as_float(x[2 * k]) * inv, __uint_as_float(x[2 * k + 1]) * inv) : 0u;
+        store_units(dst + (c >> 1) * kChunk, r, 4 * (c & 1), v[0], v[1]);
+        store_units(dst + (c >> 1) * kChunk, r, 4 * (c & 1) + 2, v[2], v[3]);
       }
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&mi.acc_empty[buf]);
       if (part == 0) {
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const uint32_t v[4] = {rope[u].x, rope[u].y, rope[u].z, rope[u].w};
-          uint4 t;
-          uint32_t* const o = reinterpret_cast<uint32_t*>(&t);
+        for (int u = 0; u < 8; u += 2) {
+          const uint32_t v[8] = {rope[u].x, rope[u].y, rope[u].z, rope[u].w, rope[u + 1].x, rope[u + 1].y, rope[u + 1].z, rope[u + 1].w};
+          uint4 t[2];
+          uint32_t* const o = reinterpret_cast<uint32_t*>(t);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
+          for (int k = 0; k < 8; ++k)
             o[k] = r < valid ? pack_f16(__uint_as_float(v[k] << 16) * inv, __uint_as_float(v[k] & 0xFFFF0000u) * inv) : 0u;
-          *reinterpret_cast<uint4*>(dst + 2 * kChunk + ((u ^ (r & 7)) * 16)) = t;
+          store_units(dst + 2 * kChunk, r, u, t[0], t[1]);
         }
       }
       if (r == 0) (part == 0 ? w.scale[tile * H + h].x : w.scale[tile * H + h].y) = static_cast<float>(f);
@@ -684,7 +693,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
       if (it < 0) return false;
       item_of(p, plan.pairs, group, it, &pc->pair, &pc->head);
       pc->t0 = 0;
-      pc->n = static_cast<int>(w.step0[pc->pair + 1] - w.step0[pc->pair]);
+      pc->n = 0x7FFFFFFF;
       pc->first = pc->last = true;
     }
     pc->pr = w.pair[pc->pair];
@@ -749,7 +758,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
         const int n = steps_of(pc, i), other = steps_of(pc, 1 - i);
         // S = Q . K^T of the next step
         auto scores = [&]() {
-#pragma unroll 1
+#pragma unroll
           for (int c = 0; c < 3; ++c) {
             if (!wait(&mi.full_k[rk.s], rk.phase)) return false;
             tc_fence_after();
@@ -823,35 +832,31 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
       }
       float a = 0.f;
       if (n > 0) {
-        // the warp's 32 rows of Q in fp16: lane l holds values 2l, 2l + 1 of each 64 of a row
-        const uint32_t* const src = reinterpret_cast<const uint32_t*>(p.q);
-#pragma unroll 1
-        for (int k0 = 0; k0 < 32; k0 += 8) {
-          uint32_t v[8][3];
+        // the warp's 32 rows of Q in fp16: lane l holds values 2l, 2l + 1 of each 64 of a row; all
+        // of them are in flight at once
+        const uint32_t* const src = reinterpret_cast<const uint32_t*>(p.q) +
+                                    (static_cast<int64_t>(pc.pr.tok0 + i * kRowsT + qd * 32) * p.H + pc.head) * 96 + lane;
+        const int have = pc.pr.ntok - i * kRowsT - qd * 32;
+        uint32_t v[32][3];
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int j = i * kRowsT + qd * 32 + k0 + k;
-            const bool have = j < pc.pr.ntok;
-            const uint32_t* const q = src + (static_cast<int64_t>(pc.pr.tok0 + (have ? j : 0)) * p.H + pc.head) * 96;
+        for (int k = 0; k < 32; ++k)
 #pragma unroll
-            for (int c = 0; c < 3; ++c) v[k][c] = have ? q[32 * c + lane] : 0u;
-          }
+          for (int c = 0; c < 3; ++c) v[k][c] = k < have ? src[static_cast<int64_t>(k) * p.H * 96 + 32 * c] : 0u;
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const int rr = qd * 32 + k0 + k;
-            float top = 0.f;
+        for (int k = 0; k < 32; ++k) {
+          const int rr = qd * 32 + k;
+          float top = 0.f;
 #pragma unroll
-            for (int c = 0; c < 3; ++c)
-              top = fmaxf(top, fmaxf(finite_abs(__uint_as_float(v[k][c] << 16)), finite_abs(__uint_as_float(v[k][c] & 0xFFFF0000u))));
-            top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-            const int f = scale_exponent(top);
-            const float inv = pow2(-f);
+          for (int c = 0; c < 3; ++c)
+            top = fmaxf(top, fmaxf(finite_abs(__uint_as_float(v[k][c] << 16)), finite_abs(__uint_as_float(v[k][c] & 0xFFFF0000u))));
+          top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+          const int f = scale_exponent(top);
+          const float inv = pow2(-f);
 #pragma unroll
-            for (int c = 0; c < 3; ++c)
-              *reinterpret_cast<uint32_t*>(sQ + i * kQTile + c * kChunk + rr * 128 + (((lane >> 2) ^ (rr & 7)) * 16) + (lane & 3) * 4) =
-                  pack_f16(__uint_as_float(v[k][c] << 16) * inv, __uint_as_float(v[k][c] & 0xFFFF0000u) * inv);
-            if (lane == k0 + k) a = p.scale_log2 * pow2(f);
-          }
+          for (int c = 0; c < 3; ++c)
+            *reinterpret_cast<uint32_t*>(sQ + i * kQTile + c * kChunk + rr * 128 + (((lane >> 2) ^ (rr & 7)) * 16) + (lane & 3) * 4) =
+                pack_f16(__uint_as_float(v[k][c] << 16) * inv, __uint_as_float(v[k][c] & 0xFFFF0000u) * inv);
+          if (lane == k) a = p.scale_log2 * pow2(f);
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -971,9 +976,13 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
             nan |= v0 != v0 || v1 != v1;
             v[k] = pack2(v0, v1);
           }
-          uint4* const dst = reinterpret_cast<uint4*>(p.out + row * 128 + 16 * c);
-          dst[0] = make_uint4(v[0], v[1], v[2], v[3]);
-          dst[1] = make_uint4(v[4], v[5], v[6], v[7]);
+          __nv_bfloat16* const dst = p.out + row * 128 + 16 * c;
+          if ((reinterpret_cast<uintptr_t>(p.out) & 16) == 0) {
+            store32(dst, make_uint4(v[0], v[1], v[2], v[3]), make_uint4(v[4], v[5], v[6], v[7]));
+          } else {
+            reinterpret_cast<uint4*>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
+            reinterpret_cast<uint4*>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+          }
         } else if (real && n > 0) {
           float4* const dst = reinterpret_cast<float4*>(w.o + (slot * kPair + tok) * 128 + 16 * c);
 #pragma unroll
@@ -1003,52 +1012,62 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
 }
 
 // ---------------------------------------------------------------- merge (shares)
-// A row of an item from its pieces, in the order of their steps; a warp per row.
-constexpr int kMergeThreads = 128;
+// Rows of an item from its pieces, in the order of their steps; eight rows a warp, so that their
+// loads are in flight together.
+constexpr int kMergeThreads = 128, kMergeRows = 8;
 
 __global__ void __launch_bounds__(kMergeThreads) merge_expanded_kernel(const __grid_constant__ Params p, int blocks) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Ws& w = p.ws;
-  const Plan plan = *w.plan;
-  const int lane = threadIdx.x & 31;
-  const int64_t all = plan.steps * p.H;
-  for (int item = blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5); item < plan.merges * kPair;
+  const int merges = w.plan->merges, lane = threadIdx.x & 31;
+  const int64_t all = w.plan->steps * p.H;
+  for (int item = blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5); item < merges * (kPair / kMergeRows);
        item += gridDim.x * (kMergeThreads / 32)) {
-    const Merge mg = w.merge[item / kPair];
+    const Merge mg = w.merge[item / (kPair / kMergeRows)];
     const Pair pr = w.pair[mg.pair];
-    const int tok = item % kPair;
+    const int tok = item % (kPair / kMergeRows) * kMergeRows;
     if (tok >= pr.ntok) continue;
-    float m = kUnset;
+    float m[kMergeRows], l[kMergeRows];
+    float4 o[kMergeRows];
+#pragma unroll
+    for (int r = 0; r < kMergeRows; ++r) m[r] = kUnset, l[r] = 0.f, o[r] = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int k = mg.first; k <= mg.last; ++k) {
-      int64_t x, y;
-      share(all, k, blocks, &x, &y);
-      if (x >= y) continue;
-      const float2 v = w.ml[static_cast<int64_t>(2 * k + (k == mg.first)) * kPair + tok];
-      if (v.y != 0.f) m = fmaxf(m, v.x);
-    }
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-    for (int k = mg.first; k <= mg.last; ++k) {
-      int64_t x, y;
-      share(all, k, blocks, &x, &y);
-      if (x >= y) continue;
+      if (all < blocks) {      // with fewer steps than blocks some shares are empty
+        int64_t x, y;
+        share(all, k, blocks, &x, &y);
+        if (x >= y) continue;
+      }
       const int64_t at = static_cast<int64_t>(2 * k + (k == mg.first)) * kPair + tok;
-      const float2 v = w.ml[at];
-      if (v.y == 0.f) continue;
-      const float4 c = reinterpret_cast<const float4*>(w.o + at * 128)[lane];
-      const float f = ex2_approx(v.x - m);
-      l = fmaf(v.y, f, l);
-      o.x = fmaf(c.x, f, o.x);
-      o.y = fmaf(c.y, f, o.y);
-      o.z = fmaf(c.z, f, o.z);
-      o.w = fmaf(c.w, f, o.w);
+      float2 v[kMergeRows];
+      float4 c[kMergeRows];
+#pragma unroll
+      for (int r = 0; r < kMergeRows; ++r) {
+        v[r] = w.ml[at + r];
+        c[r] = reinterpret_cast<const float4*>(w.o + (at + r) * 128)[lane];
+      }
+#pragma unroll
+      for (int r = 0; r < kMergeRows; ++r) {
+        if (v[r].y == 0.f) continue;          // no token of the row in this piece: nothing was stored
+        const float now = fmaxf(m[r], v[r].x), f0 = ex2_approx(m[r] - now), f1 = ex2_approx(v[r].x - now);
+        m[r] = now;
+        l[r] = fmaf(l[r], f0, v[r].y * f1);
+        o[r].x = fmaf(o[r].x, f0, c[r].x * f1);
+        o[r].y = fmaf(o[r].y, f0, c[r].y * f1);
+        o[r].z = fmaf(o[r].z, f0, c[r].z * f1);
+        o[r].w = fmaf(o[r].w, f0, c[r].w * f1);
+      }
     }
-    const float inv = l != 0.f ? 1.f / l : 0.f;
-    const int64_t row = static_cast<int64_t>(pr.tok0 + tok) * p.H + mg.head;
-    reinterpret_cast<uint2*>(p.out + row * 128)[lane] =
-        l != 0.f ? make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv)) : make_uint2(0u, 0u);
-    const bool nan = inv == inv && !(o.x == o.x && o.y == o.y && o.z == o.z && o.w == o.w);
-    if (__any_sync(0xffffffffu, nan) && lane < 2) redo_half_row(p, pr.tile0, row, mg.head, p.positions[pr.tok0 + tok], lane);
+#pragma unroll
+    for (int r = 0; r < kMergeRows; ++r) {
+      if (tok + r >= pr.ntok) continue;
+      const float inv = l[r] != 0.f ? 1.f / l[r] : 0.f;
+      const int64_t row = static_cast<int64_t>(pr.tok0 + tok + r) * p.H + mg.head;
+      reinterpret_cast<uint2*>(p.out + row * 128)[lane] =
+          l[r] != 0.f ? make_uint2(pack2(o[r].x * inv, o[r].y * inv), pack2(o[r].z * inv, o[r].w * inv)) : make_uint2(0u, 0u);
+      const bool nan = inv == inv && l[r] != 0.f && !(o[r].x == o[r].x && o[r].y == o[r].y && o[r].z == o[r].z && o[r].w == o[r].w);
+      if (__any_sync(0xffffffffu, nan) && lane < 2) redo_half_row(p, pr.tile0, row, mg.head, p.positions[pr.tok0 + tok + r], lane);
+      __syncwarp();
+    }
   }
 }
 
