@@ -554,11 +554,9 @@ struct Piece {
 };
 
 // Items in order: a group of heads, the pairs, the heads of the group.
-__device__ __forceinline__ void item_of(const Params& p, int pairs, int group, int64_t it, int* pair, int* head) {
-  const int64_t per = static_cast<int64_t>(group) * pairs;
-  const int g = static_cast<int>(it / per);
-  const int rest = static_cast<int>(it - g * per);
-  const int in = p.H - g * group < group ? p.H - g * group : group;
+__device__ __forceinline__ void item_of(const Params& p, uint32_t pairs, uint32_t group, uint32_t it, int* pair, int* head) {
+  const uint32_t per = group * pairs, g = it / per, rest = it - g * per;   // pairs * H stays below 2^31
+  const uint32_t in = p.H - g * group < group ? p.H - g * group : group;
   *pair = rest / in;
   *head = g * group + rest % in;
 }
@@ -845,12 +843,10 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
 #pragma unroll
         for (int k = 0; k < 32; ++k) {
           const int rr = qd * 32 + k;
-          float top = 0.f;
-#pragma unroll
-          for (int c = 0; c < 3; ++c)
-            top = fmaxf(top, fmaxf(finite_abs(__uint_as_float(v[k][c] << 16)), finite_abs(__uint_as_float(v[k][c] & 0xFFFF0000u))));
-          top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-          const int f = scale_exponent(top);
+          // magnitudes of bf16 pairs compare as integers (a row with an infinity is lost anyway)
+          uint32_t top = __vmaxu2(__vmaxu2(v[k][0] & 0x7FFF7FFFu, v[k][1] & 0x7FFF7FFFu), v[k][2] & 0x7FFF7FFFu);
+          top = __reduce_max_sync(0xffffffffu, top >> 16 > (top & 0xFFFFu) ? top >> 16 : top & 0xFFFFu);
+          const int f = scale_exponent(__uint_as_float(top << 16));
           const float inv = pow2(-f);
 #pragma unroll
           for (int c = 0; c < 3; ++c)
@@ -965,28 +961,39 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
       const int64_t slot = 2 * blockIdx.x + (pc.first ? 1 : 0);    // head pieces 0, tail pieces 1
       bool nan = false;
 #pragma unroll 1
-      for (int c = 0; c < 8; ++c) {
-        float o[16];
-        if (n > 0) tmem_ld16(to + 16 * c, o);
-        if (real && whole) {
-          uint32_t v[8];
+      for (int c = 0; c < 4; ++c) {
+        uint32_t o[32];
+        if (n > 0) {
+          tmem_ld_32cols(to + 32 * c, o);
+          tmem_ld_wait(o);
+        } else {
 #pragma unroll
-          for (int k = 0; k < 8; ++k) {
-            const float v0 = l != 0.f ? o[2 * k] * inv : 0.f, v1 = l != 0.f ? o[2 * k + 1] * inv : 0.f;
-            nan |= v0 != v0 || v1 != v1;
-            v[k] = pack2(v0, v1);
+          for (int k = 0; k < 32; ++k) o[k] = 0u;
+        }
+        if (real && whole) {
+          uint4 v[4];
+          uint32_t* const u = reinterpret_cast<uint32_t*>(v);
+          float zero = 0.f;        // NaN if a value is
+#pragma unroll
+          for (int k = 0; k < 16; ++k) {
+            const float v0 = __uint_as_float(o[2 * k]) * inv, v1 = __uint_as_float(o[2 * k + 1]) * inv;
+            zero = fmaf(v0, 0.f, fmaf(v1, 0.f, zero));
+            u[k] = pack2(v0, v1);
           }
-          __nv_bfloat16* const dst = p.out + row * 128 + 16 * c;
+          nan |= zero != 0.f;
+          __nv_bfloat16* const dst = p.out + row * 128 + 32 * c;
           if ((reinterpret_cast<uintptr_t>(p.out) & 16) == 0) {
-            store32(dst, make_uint4(v[0], v[1], v[2], v[3]), make_uint4(v[4], v[5], v[6], v[7]));
+            store32(dst, v[0], v[1]);
+            store32(dst + 16, v[2], v[3]);
           } else {
-            reinterpret_cast<uint4*>(dst)[0] = make_uint4(v[0], v[1], v[2], v[3]);
-            reinterpret_cast<uint4*>(dst)[1] = make_uint4(v[4], v[5], v[6], v[7]);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) reinterpret_cast<uint4*>(dst)[k] = v[k];
           }
         } else if (real && n > 0) {
-          float4* const dst = reinterpret_cast<float4*>(w.o + (slot * kPair + tok) * 128 + 16 * c);
+          float* const dst = w.o + (slot * kPair + tok) * 128 + 32 * c;
 #pragma unroll
-          for (int k = 0; k < 4; ++k) dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          for (int k = 0; k < 32; k += 8)
+            store32(dst + k, make_uint4(o[k], o[k + 1], o[k + 2], o[k + 3]), make_uint4(o[k + 4], o[k + 5], o[k + 6], o[k + 7]));
         }
         __syncwarp();
       }
