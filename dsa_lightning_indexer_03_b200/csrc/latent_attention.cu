@@ -293,38 +293,25 @@ __device__ __forceinline__ Fp4Chunk fp4_load(const uint8_t* row, int c) {
   return f;
 }
 
-// e4m3 scale as bf16 in both halves (exact: 4 significant bits)
-__device__ __forceinline__ uint32_t scale_bf16x2(uint32_t c) {
-  const uint32_t e = (c >> 3) & 15u, m = c & 7u;
-  const float v = e ? __uint_as_float(((e + 120u) << 23) | (m << 20)) : static_cast<float>(m) * 0x1p-9f;
-  return __byte_perm(__float_as_uint(v), 0, 0x3232);
-}
-
-__device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
+__device__ __forceinline__ uint32_t mul_f16x2(uint32_t a, uint32_t b) {
   uint32_t d;
-  asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+  asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
   return d;
 }
 
-// Eight codes as eight bf16 values times their scale.  The high and the low byte of a magnitude's
-// bf16 form are looked up with the three magnitude bits as byte selectors; the two sign bits of a
-// pair reach bits 15 and 31 through one multiplication (its partial products do not overlap).
+// Eight codes as eight fp16 values times their scale (exact: at most 2 + 4 significant bits, and
+// magnitudes from 2^-10 to 2,880)
 __device__ __forceinline__ uint4 fp4_word(uint32_t w, uint32_t s2) {
-  const uint32_t mag = w & 0x77777777u, sgn = w & 0x88888888u;
   uint4 r;
-  uint32_t* const o = reinterpret_cast<uint32_t*>(&r);
-#pragma unroll
-  for (int hlf = 0; hlf < 2; ++hlf) {
-    const uint32_t sel = hlf ? mag >> 16 : mag;
-    const uint32_t hi = __byte_perm(0x3F3F3F00u, 0x40404040u, sel), lo = __byte_perm(0xC0800000u, 0xC0804000u, sel);
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const uint32_t v = __byte_perm(lo, hi, k ? 0x7362 : 0x5140);
-      const uint32_t b = __byte_perm(sgn, 0, 0x4440 + 2 * hlf + k);
-      o[2 * hlf + k] = mul_bf16x2(v ^ ((b * 0x01001000u) & 0x80008000u), s2);
-    }
-  }
-  return r;
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\t"
+      "mov.b32 {b0, b1, b2, b3}, %4;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %2, b2;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+      : "r"(w));
+  return make_uint4(mul_f16x2(r.x, s2), mul_f16x2(r.y, s2), mul_f16x2(r.z, s2), mul_f16x2(r.w, s2));
 }
 
 // The chunk as a 128-byte row of a swizzled tile: 16-byte unit u of row r at unit u ^ (r & 7)
@@ -332,7 +319,8 @@ __device__ __forceinline__ void fp4_store(uint8_t* dst_row, int r, const Fp4Chun
   const uint32_t w[8] = {f.a.x, f.a.y, f.a.z, f.a.w, f.b.x, f.b.y, f.b.z, f.b.w};
 #pragma unroll
   for (int k = 0; k < 4; ++k) {
-    const uint32_t s2 = scale_bf16x2((f.sc >> (8 * k)) & 0xFFu);
+    // e4m3 bits moved to fp16's fields read as 2^-8 of the scale, subnormals too
+    const uint32_t s2 = mul_f16x2(((f.sc >> (8 * k)) & 0x7Fu) * 0x00800080u, 0x5C005C00u);
 #pragma unroll
     for (int j = 0; j < 2; ++j)
       *reinterpret_cast<uint4*>(dst_row + (((2 * k + j) ^ (r & 7)) * 16)) = fp4_word(w[2 * k + j], s2);
@@ -350,6 +338,7 @@ struct alignas(16) Misc {
   int pad;
   alignas(16) float nm[kRows];       // minus the reference of each row (log2 units)
   alignas(16) float f[kRows];        // factor of a raised reference; at the end 1 / sum
+  alignas(16) float qs[2][kRows];    // 4-bit cache: each row's factor to log2 units, pieces in turn
   alignas(16) int limit[kRows];      // last position the row attends to
   alignas(16) float red[kSoftWarps][kCols];
   int spoiled[kRows];                // the row's sums hold a NaN that its weights do not
@@ -423,7 +412,7 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
       mbar_init(&mi.zero_req[s], 1);
       mbar_init(&mi.zeroed[s], 1);
     }
-    mbar_init(&mi.q_full, 1);
+    mbar_init(&mi.q_full, FP4 ? 128 : 1);
     mbar_init(&mi.q_empty, 1);
     mbar_init(&mi.s_full, 1);
     mbar_init(&mi.s_empty, kSoftWarps);
@@ -480,12 +469,6 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
     uint32_t it = 0;        // stages of the warp's ring so far
     uint32_t segs = 0;      // pieces so far
     bool ok = true;
-    auto q_load = [&]() {
-      if (segs > 0 && !mbar_wait(&mi.q_empty, (segs - 1) & 1, wc)) return false;
-      mbar_arrive_expect_tx(&mi.q_full, kQBytes);
-      for (int c = 0; c < 9; ++c) tma_load_2d(sQ + c * kQChunk, &tmQ, &mi.q_full, 64 * c, pc.g.row0);
-      return true;
-    };
     if constexpr (FP4) {
       const int i = threadIdx.x & 127;     // token of the tile (scores), token and half (values)
       const bool scores = warp < 4;
@@ -506,7 +489,31 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
           return base + static_cast<int64_t>(pos) * kLatRow4;
         };
         if (scores) {
-          if (i == 0) ok = q_load();
+          // Q with its latent part in fp16 (the type of the cache's values) and its rope part in
+          // bf16, both times a power of two that fits the row into fp16
+          if (segs > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait(&mi.q_empty, (segs - 1) & 1, wc)))) break;
+          const int lane_ = threadIdx.x & 31;
+          const uint32_t* const qsrc = reinterpret_cast<const uint32_t*>(p.q) + static_cast<int64_t>(pc.g.row0) * (kLatDim / 2) + lane_;
+#pragma unroll 2
+          for (int rr = warp; rr < kRows; rr += 4) {
+            uint32_t v[9], top = 0u;
+#pragma unroll
+            for (int c = 0; c < 9; ++c) v[c] = rr < pc.g.nrows ? qsrc[rr * (kLatDim / 2) + 32 * c] : 0u;
+#pragma unroll
+            for (int c = 0; c < 9; ++c) top = __vmaxu2(top, v[c] & 0x7FFF7FFFu);
+            top = __reduce_max_sync(0xffffffffu, top >> 16 > (top & 0xFFFFu) ? top >> 16 : top & 0xFFFFu);
+            const int f = scale_exponent(__uint_as_float(top << 16));
+            const float inv = pow2(-f);
+#pragma unroll
+            for (int c = 0; c < 9; ++c) {
+              const float lo = __uint_as_float(v[c] << 16) * inv, hi = __uint_as_float(v[c] & 0xFFFF0000u) * inv;
+              *reinterpret_cast<uint32_t*>(sQ + c * kQChunk + rr * 128 + (((lane_ >> 2) ^ (rr & 7)) * 16) + (lane_ & 3) * 4) =
+                  c < 8 ? pack_f16(lo, hi) : pack2(lo, hi);
+            }
+            if (lane_ == 0) mi.qs[segs & 1][rr] = p.scale_log2 * pow2(f);
+          }
+          fence_proxy_async_smem();
+          mbar_arrive(&mi.q_full);
           ++segs;
           auto prefetch = [&](int t) {
             if (t >= pc.t0 + pc.n) return;
@@ -572,12 +579,13 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
           }
         }
       }
-      if (scores && i == 0 && !ok && segs > 0) drain(&mi.q_full, (segs - 1) & 1);
     } else if (warp == 0 && lane == 0) {
       // scores: nine 64-value chunks of a tile
       while (ok && walk.next(&pc)) {
         if (pc.g.ntok == 0) continue;
-        ok = q_load();
+        if (segs > 0 && !(ok = mbar_wait(&mi.q_empty, (segs - 1) & 1, wc))) break;
+        mbar_arrive_expect_tx(&mi.q_full, kQBytes);
+        for (int c = 0; c < 9; ++c) tma_load_2d(sQ + c * kQChunk, &tmQ, &mi.q_full, 64 * c, pc.g.row0);
         ++segs;
         for (int t = pc.t0; t < pc.t0 + pc.n && ok; ++t) {
           const bool two = tile_tokens(pc.g, t) > 64;
@@ -661,7 +669,7 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
     const uint32_t tlane = tmem + (static_cast<uint32_t>(qd * 32) << 16);
     const int wtid = (warp - R::kFill - 4 * wg) * 32 + lane;
     const int bar_id = 1 + wg;
-    uint32_t done = 0;      // tiles so far
+    uint32_t done = 0, segs = 0;      // tiles and pieces with tokens so far
     // A wait that ran out is skipped from then on, but the walk goes on to its end: the warps of
     // a third meet at named barriers and none may leave the others there.  The results are then
     // worthless, and the error word says so.
@@ -730,13 +738,15 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
 #pragma unroll
           for (int c = 0; c < kCols / 2; ++c) y[c] = make_float2(x[2 * c], x[2 * c + 1]);
         };
-        const float2 scale2 = make_float2(p.scale_log2, p.scale_log2);
+        const float4* const qs4 = reinterpret_cast<const float4*>(mi.qs[segs & 1] + c0);
         auto shift = [&]() {
 #pragma unroll
           for (int c = 0; c < kCols / 4; ++c) {
             const float4 m = nm4[c];
-            y[2 * c] = ffma2(y[2 * c], scale2, make_float2(m.x, m.y));
-            y[2 * c + 1] = ffma2(y[2 * c + 1], scale2, make_float2(m.z, m.w));
+            float4 k = make_float4(p.scale_log2, p.scale_log2, p.scale_log2, p.scale_log2);
+            if (FP4) k = qs4[c];
+            y[2 * c] = ffma2(y[2 * c], make_float2(k.x, k.y), make_float2(m.x, m.y));
+            y[2 * c + 1] = ffma2(y[2 * c + 1], make_float2(k.z, k.w), make_float2(m.z, m.w));
           }
         };
         if (nc > 0) {
@@ -758,7 +768,7 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
           if (wtid < nc) {
             float v = -INFINITY;
             for (int k = 0; k < 4; ++k) v = fmaxf(v, mi.red[4 * wg + k][wtid]);
-            v *= p.scale_log2;
+            v *= FP4 ? mi.qs[segs & 1][c0 + wtid] : p.scale_log2;
             const float old = -mi.nm[c0 + wtid];
             const float now = v > old + 8.f ? v : old;
             mi.nm[c0 + wtid] = -now;
@@ -792,15 +802,16 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&mi.s_empty);
-        // weights: 2^y, summed before their rounding to bf16 (lse keeps fp32's precision; out
-        // gets one rounding of up to 2^-8 a weight, the operand type of the product)
+        // weights: 2^y, summed before their rounding to the values' type, the operand type of the
+        // product (lse keeps fp32's precision; out gets one rounding a weight, of up to 2^-8 in
+        // bf16; in fp16 2^-11, and 2^-25 where a weight is below 2^-14 of the largest)
         uint32_t pk[kCols / 2];
         if (nc > 0) {
 #pragma unroll
           for (int c = 0; c < kCols / 2; ++c) {
             const float2 e = make_float2(ex2_approx(y[c].x), ex2_approx(y[c].y));
             l[c] = __fadd2_rn(l[c], e);
-            pk[c] = pack2(e.x, e.y);
+            pk[c] = FP4 ? pack_f16(e.x, e.y) : pack2(e.x, e.y);
           }
         }
         // the weights' place in shared memory is free once the previous tile's product is done
@@ -817,6 +828,7 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(&mi.p_full);
       }
+      if (g.ntok > 0) ++segs;
       // the rows' sums over the 128 threads
       named_bar_sync(bar_id, 128);
       {
@@ -897,7 +909,7 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
         const uint32_t q_lo = desc_lo(smem_u32(sQ), 16), r_lo = desc_lo(smem_u32(sRing), 16);   // K-major
         while (ok && walk.next(&pc)) {
           if (pc.g.ntok == 0) continue;
-          const uint32_t idesc = umma_idesc_bf16(128, (pc.g.nrows + 15) / 16 * 16);
+          const int n16 = (pc.g.nrows + 15) / 16 * 16;
           if (!(ok = wait(&mi.q_full, segs & 1))) break;
           ++segs;
           for (int t = 0; t < pc.n && ok; ++t, ++nth) {
@@ -908,6 +920,7 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
               if (!(ok = wait(&mi.full_s[rg.s], rg.phase))) break;
               tc_fence_after();
               const uint32_t a = r_lo + rg.s * (kStage >> 4), b = q_lo + c * (kQChunk >> 4);
+              const uint32_t idesc = FP4 && c < 8 ? idesc_f16(128, n16) : umma_idesc_bf16(128, n16);
 #pragma unroll
               for (int k = 0; k < 4; ++k) umma_lo(tmem + kTmemS, a + 2 * k, b + 2 * k, idesc, (c | k) != 0, leader);
               commit(&mi.empty_s[rg.s]);
@@ -925,7 +938,8 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
         while (ok && walk.next(&pc)) {
           const Group& g = pc.g;
           if (g.ntok == 0) continue;
-          const uint32_t idesc = umma_idesc_bf16(128, (g.nrows + 15) / 16 * 16) | (1u << 15) | (1u << 16);
+          const int n16 = (g.nrows + 15) / 16 * 16;
+          const uint32_t idesc = (FP4 ? idesc_f16(128, n16) : umma_idesc_bf16(128, n16)) | (1u << 15) | (1u << 16);
           for (int t = 0; t < pc.n && ok; ++t, ++nth) {
             const int v = tile_tokens(g, pc.t0 + t), halves = v > 64 ? 2 : 1;
             const bool zero = !FP4 && pc.last && t == pc.n - 1 && (v & 15);

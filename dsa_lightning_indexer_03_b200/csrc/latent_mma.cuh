@@ -119,4 +119,25 @@ __device__ __forceinline__ void tmem_st16(uint32_t a, const float (&x)[16]) {
       : "memory");
 }
 
+// kind::f16 with fp16 A and B, fp32 accumulator, both K-major
+__host__ __device__ constexpr uint32_t idesc_f16(int M, int N) {
+  return (1u << 4) | (static_cast<uint32_t>(N >> 3) << 17) | (static_cast<uint32_t>(M >> 4) << 24);
+}
+
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+
+// 2^e, e in [-126, 127]
+__device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
+
+// Exponent f of the scale 2^f that brings a largest magnitude of `top` to below 2^15, so that
+// fp16 holds it; nothing is lifted by more than 2^14.
+__device__ __forceinline__ int scale_exponent(float top) {
+  const int e = static_cast<int>((__float_as_uint(top) >> 23) & 0xFF) - 127;
+  return (e < 0 ? 0 : e) - 14;
+}
+
 }  // namespace dsa
