@@ -23,8 +23,8 @@
 //   warps 4-15  softmax: a thread per token, a third of the rows each.  The reference m of a row
 //               is its running maximum, raised only when a score exceeds it by more than 8 (log2
 //               units, so weights stay below 256): most tiles then need no maximum over the
-//               tokens, which lie across threads, only a vote.  Sums are kept per thread and
-//               added up at the end.  Weights go to shared memory as bf16 (the MMA's operand).
+//               tokens, which lie across threads, only a vote.  Sums are taken over the warp
+//               in every tile, over the warps at the end.  Weights go to shared memory as bf16 (the MMA's operand).
 //   warp 16     (of a warpgroup that otherwise idles) issues the MMAs: S(t+1) before the values of t, so that the softmax of a tile
 //               runs under the MMAs of its neighbours.
 // Work: plan_kernel lists the groups and their tiles; the blocks take equal shares of all tiles
@@ -279,17 +279,21 @@ __device__ __forceinline__ void tmem_ld32(uint32_t a, float (&x)[kCols]) {
 }
 
 // ---------------------------------------------------------------- 4-bit rows
-// 64 values of a row: eight words of codes (first value in the lowest nibble) and four scales
-struct Fp4Chunk {
-  uint4 a, b;
+// 32 values of a row: four words of codes (first value in the lowest nibble) and two scales.  Four
+// neighbouring lanes take 128 values of a row, so that a load touches eight lines, not 32 (with a
+// row a lane the loads alone kept the memory pipe busy for 9,000 cycles a tile).
+struct Fp4Raw {
+  uint4 w;
   uint32_t sc;
 };
 
-__device__ __forceinline__ Fp4Chunk fp4_load(const uint8_t* row, int c) {
-  Fp4Chunk f;
-  f.a = *reinterpret_cast<const uint4*>(row + 32 * c);
-  f.b = *reinterpret_cast<const uint4*>(row + 32 * c + 16);
-  f.sc = *reinterpret_cast<const uint32_t*>(row + kLatCodes + 4 * c);
+__device__ __forceinline__ Fp4Raw fp4_load(const uint8_t* base, int pos, int group) {
+  Fp4Raw f = {};
+  if (pos >= 0) {
+    const uint8_t* const row = base + static_cast<int64_t>(pos) * kLatRow4;
+    f.w = *reinterpret_cast<const uint4*>(row + 16 * group);
+    f.sc = *reinterpret_cast<const uint16_t*>(row + kLatCodes + 2 * group);
+  }
   return f;
 }
 
@@ -314,16 +318,22 @@ __device__ __forceinline__ uint4 fp4_word(uint32_t w, uint32_t s2) {
   return make_uint4(mul_f16x2(r.x, s2), mul_f16x2(r.y, s2), mul_f16x2(r.z, s2), mul_f16x2(r.w, s2));
 }
 
-// The chunk as a 128-byte row of a swizzled tile: 16-byte unit u of row r at unit u ^ (r & 7)
-__device__ __forceinline__ void fp4_store(uint8_t* dst_row, int r, const Fp4Chunk& f) {
-  const uint32_t w[8] = {f.a.x, f.a.y, f.a.z, f.a.w, f.b.x, f.b.y, f.b.z, f.b.w};
+// The 32 values as four 16-byte units of a 128-byte row r of a swizzled chunk (unit u at unit
+// u ^ (r & 7)): the row's first four or last four (`upper`).  The lanes of a row's second chunk
+// (`second`) store their units in another order, so that eight lanes never meet in a bank.
+__device__ __forceinline__ void fp4_store(uint8_t* row, int r, bool upper, bool second, Fp4Raw f) {
+  if (second) {
+    f.w = make_uint4(f.w.z, f.w.w, f.w.x, f.w.y);
+    f.sc = (f.sc >> 8) | (f.sc << 8);
+  }
+  const uint32_t w[4] = {f.w.x, f.w.y, f.w.z, f.w.w};
+  const int u0 = (upper ? 4 : 0) ^ (second ? 2 : 0) ^ (r & 7);
 #pragma unroll
-  for (int k = 0; k < 4; ++k) {
+  for (int k = 0; k < 2; ++k) {
     // e4m3 bits moved to fp16's fields read as 2^-8 of the scale, subnormals too
     const uint32_t s2 = mul_f16x2(((f.sc >> (8 * k)) & 0x7Fu) * 0x00800080u, 0x5C005C00u);
 #pragma unroll
-    for (int j = 0; j < 2; ++j)
-      *reinterpret_cast<uint4*>(dst_row + (((2 * k + j) ^ (r & 7)) * 16)) = fp4_word(w[2 * k + j], s2);
+    for (int j = 0; j < 2; ++j) *reinterpret_cast<uint4*>(row + ((u0 ^ (2 * k + j)) * 16)) = fp4_word(w[2 * k + j], s2);
   }
 }
 
@@ -386,9 +396,48 @@ __device__ __forceinline__ int tile_tokens(const Group& g, int t) {
   return left < kTile ? left : kTile;
 }
 
+// A thread's dims (tok, 128 + tok, ...) of 32 rows of a finished piece: out = sums * f, or the sums
+// as they are to a slot of the workspace.  Not inlined: its addresses, live across the tiles'
+// loop, would push the loop's own values out of the registers.
+template <bool FP4>
+__device__ __noinline__ void write_sums(const Params& p, const float* f, int* spoiled, uint32_t tlane, int tok, int c0,
+                                        int row0, int nrows, bool any, float* slot) {
+  const int lane = tok & 31;
+#pragma unroll 1
+  for (int u = 0; u < 8; ++u) {
+    const int j = u & 3, cb = c0 + (u >> 2) * 16;         // block of dims, first of 16 rows
+    if (cb >= nrows) break;
+    float o[16];
+    if (any) tmem_ld16(tlane + j * kRows + cb, o);
+    const int dim = 128 * j + tok;
+    if (!slot) {
+      // even lanes keep row c, odd lanes row c + 1, each with its pair of dims
+      __nv_bfloat16* const ob = p.out + static_cast<int64_t>(row0 + cb + (lane & 1)) * kLatV + (dim & ~1);
+#pragma unroll
+      for (int c = 0; c < 16; c += 2) {
+        const float i0 = f[cb + c], i1 = f[cb + c + 1];
+        const float v0 = i0 != 0.f ? o[c] * i0 : 0.f, v1 = i1 != 0.f ? o[c + 1] * i1 : 0.f;
+        if (!FP4) {
+          if (v0 != v0 && i0 == i0) spoiled[cb + c] = 1;
+          if (v1 != v1 && i1 == i1) spoiled[cb + c + 1] = 1;
+        }
+        const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? v0 : v1, 1);
+        const uint32_t pr = lane & 1 ? pack2(got, v1) : pack2(v0, got);
+        if (cb + c + (lane & 1) < nrows) *reinterpret_cast<uint32_t*>(ob + c * kLatV) = pr;
+      }
+    } else {
+      float* const ob = slot + static_cast<int64_t>(cb) * kLatV + dim;
+#pragma unroll
+      for (int c = 0; c < 16; ++c)
+        if (cb + c < nrows) ob[c * kLatV] = o[c];
+    }
+  }
+}
+
 template <bool FP4>
 __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
-    latent_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmC, Params p) {
+    latent_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmC,
+                            const __grid_constant__ Params p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* const sQ = smem;
@@ -470,30 +519,27 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
     uint32_t segs = 0;      // pieces so far
     bool ok = true;
     if constexpr (FP4) {
-      const int i = threadIdx.x & 127;     // token of the tile (scores), token and half (values)
       const bool scores = warp < 4;
+      const int w4 = warp & 3, sub = lane >> 2, quad = lane & 3;   // row of eight, part of a row
+      const bool upper = quad & 1, second = quad >> 1;
       while (ok && walk.next(&pc)) {
         if (pc.g.ntok == 0) continue;
         const uint8_t* const base = p.kv4 + pc.g.kv_row0 * kLatRow4;
         const int32_t* const sel = p.k_sel >= 0 ? p.idx + static_cast<int64_t>(pc.g.row0 / p.H) * p.k_sel : nullptr;
-        // cache row of token j of tile t, or null
-        auto row_of = [&](int t, int j) -> const uint8_t* {
+        // position of token j of tile t in the sequence, or -1
+        auto pos_of = [&](int t, int j) {
           const int k = t * kTile + j;
-          if (k >= pc.g.ntok) return nullptr;
-          int pos = k;
-          if (sel) {
-            pos = sel[k];
-            if (pos >= pc.g.seq_len) atomicOr(p.err, kErrBounds);
-            if (pos < 0 || pos >= pc.g.seq_len) return nullptr;
-          }
-          return base + static_cast<int64_t>(pos) * kLatRow4;
+          if (k >= pc.g.ntok) return -1;
+          if (!sel) return k;
+          const int pos = sel[k];
+          if (pos >= pc.g.seq_len) atomicOr(p.err, kErrBounds);
+          return pos < pc.g.seq_len ? pos : -1;
         };
         if (scores) {
           // Q with its latent part in fp16 (the type of the cache's values) and its rope part in
           // bf16, both times a power of two that fits the row into fp16
           if (segs > 0 && !(ok = __all_sync(0xffffffffu, mbar_wait(&mi.q_empty, (segs - 1) & 1, wc)))) break;
-          const int lane_ = threadIdx.x & 31;
-          const uint32_t* const qsrc = reinterpret_cast<const uint32_t*>(p.q) + static_cast<int64_t>(pc.g.row0) * (kLatDim / 2) + lane_;
+          const uint32_t* const qsrc = reinterpret_cast<const uint32_t*>(p.q) + static_cast<int64_t>(pc.g.row0) * (kLatDim / 2) + lane;
 #pragma unroll 2
           for (int rr = warp; rr < kRows; rr += 4) {
             uint32_t v[9], top = 0u;
@@ -507,18 +553,19 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
 #pragma unroll
             for (int c = 0; c < 9; ++c) {
               const float lo = __uint_as_float(v[c] << 16) * inv, hi = __uint_as_float(v[c] & 0xFFFF0000u) * inv;
-              *reinterpret_cast<uint32_t*>(sQ + c * kQChunk + rr * 128 + (((lane_ >> 2) ^ (rr & 7)) * 16) + (lane_ & 3) * 4) =
+              *reinterpret_cast<uint32_t*>(sQ + c * kQChunk + rr * 128 + (((lane >> 2) ^ (rr & 7)) * 16) + (lane & 3) * 4) =
                   c < 8 ? pack_f16(lo, hi) : pack2(lo, hi);
             }
-            if (lane_ == 0) mi.qs[segs & 1][rr] = p.scale_log2 * pow2(f);
+            if (lane == 0) mi.qs[segs & 1][rr] = p.scale_log2 * pow2(f);
           }
           fence_proxy_async_smem();
           mbar_arrive(&mi.q_full);
           ++segs;
           auto prefetch = [&](int t) {
             if (t >= pc.t0 + pc.n) return;
-            const uint8_t* r = row_of(t, i);
-            if (!r) return;
+            const int pos = pos_of(t, threadIdx.x & 127);
+            if (pos < 0) return;
+            const uint8_t* const r = base + static_cast<int64_t>(pos) * kLatRow4;
 #pragma unroll
             for (int k = 0; k < 4; ++k) asm volatile("prefetch.global.L2 [%0];" ::"l"(r + 128 * k));
             asm volatile("prefetch.global.L2 [%0];" ::"l"(r + kLatRow4 - 16));
@@ -526,55 +573,83 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
           prefetch(pc.t0);
           for (int t = pc.t0; t < pc.t0 + pc.n && ok; ++t) {
             prefetch(t + 1);
-            const uint8_t* r = row_of(t, i);
-            Fp4Chunk nx = {};
-            if (r) nx = fp4_load(r, 0);
-            for (int c = 0; c < 9; ++c) {
-              const Fp4Chunk cur = nx;
-              if (r && c + 1 < 8) nx = fp4_load(r, c + 1);
-              if (!(ok = acquire(mi.empty_s, it, kSStages))) break;
-              const uint32_t s = it % kSStages;
-              uint8_t* const dst = sRing + s * kStage + i * 128;
-              if (r && c < 8) {
-                fp4_store(dst, i, cur);
-              } else if (r) {
+            // the warp's 32 rows, eight at a time; two chunks (128 values) together
+            int pos[4];
 #pragma unroll
-                for (int u = 0; u < 8; ++u)
-                  *reinterpret_cast<uint4*>(dst + ((u ^ (i & 7)) * 16)) =
-                      reinterpret_cast<const uint4*>(r + kLatCodes + kLatScales)[u];
-              }   // a missing token's score is masked, whatever its row holds
+            for (int k = 0; k < 4; ++k) pos[k] = pos_of(t, 32 * w4 + 8 * k + sub);
+            Fp4Raw nx[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) nx[k] = fp4_load(base, pos[k], quad);
+#pragma unroll 1
+            for (int c = 0; c < 4; ++c) {
+              Fp4Raw cur[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) cur[k] = nx[k];
+              if (c < 3) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) nx[k] = fp4_load(base, pos[k], 4 * (c + 1) + quad);
+              }
+              const uint32_t s0 = it % kSStages, s1 = (it + 1) % kSStages;
+              if (!(ok = __all_sync(0xffffffffu, acquire(mi.empty_s, it, kSStages) && acquire(mi.empty_s, it + 1, kSStages)))) break;
+              uint8_t* const dst = sRing + (second ? s1 : s0) * kStage;
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int r = 32 * w4 + 8 * k + sub;
+                // a missing token's score is masked, whatever its row holds
+                if (pos[k] >= 0) fp4_store(dst + r * 128, r, upper, second, cur[k]);
+              }
               fence_proxy_async_smem();
-              mbar_arrive(&mi.full_s[s]);
-              ++it;
+              mbar_arrive(&mi.full_s[s0]);
+              mbar_arrive(&mi.full_s[s1]);
+              it += 2;
             }
+            if (!ok) break;
+            // the rope keys: eight lanes a row, a warp's four rows at a time
+            uint4 v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int r = 4 * k + (lane >> 3);           // of the warp's 32; lane 4 (r & 7) holds its position
+              const int a = __shfl_sync(0xffffffffu, pos[k >> 1], 4 * (r & 7));
+              v[k] = a >= 0 ? *reinterpret_cast<const uint4*>(base + static_cast<int64_t>(a) * kLatRow4 + kLatCodes + kLatScales + 16 * (lane & 7))
+                            : make_uint4(0u, 0u, 0u, 0u);
+            }
+            const uint32_t s = it % kSStages;
+            if (!(ok = __all_sync(0xffffffffu, acquire(mi.empty_s, it, kSStages)))) break;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const int r = 32 * w4 + 4 * k + (lane >> 3);
+              *reinterpret_cast<uint4*>(sRing + s * kStage + r * 128 + (((lane & 7) ^ (r & 7)) * 16)) = v[k];
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&mi.full_s[s]);
+            ++it;
           }
         } else {
           for (int t = pc.t0; t < pc.t0 + pc.n && ok; ++t) {
             const int halves = tile_tokens(pc.g, t) > 64 ? 2 : 1;
-            const int j = i & 63, part = i >> 6;
-            const uint8_t* const r0 = row_of(t, j);
-            const uint8_t* const r1 = halves == 2 ? row_of(t, 64 + j) : nullptr;
-            Fp4Chunk nx = {};
-            if (r0) nx = fp4_load(r0, part);
-            for (int k = 0; k < 4 * halves; ++k) {
-              const Fp4Chunk cur = nx;
-              const bool have = (halves == 2 && (k & 1) ? r1 : r0) != nullptr;
-              if (k + 1 < 4 * halves) {
-                const uint8_t* const rn = halves == 2 && !(k & 1) ? r1 : r0;
-                if (rn) nx = fp4_load(rn, 2 * (halves == 2 ? (k + 1) >> 1 : k + 1) + part);
-              }
-              if (!(ok = acquire(mi.empty_v, it, kVStages))) break;
-              const uint32_t s = it % kVStages;
-              uint8_t* const dst = sRingV + s * kStage + part * 8192 + j * 128;
-              if (have) {
-                fp4_store(dst, j, cur);
-              } else {
+            // the warp's 16 rows of either half
+            int pos[2][2];
 #pragma unroll
-                for (int u = 0; u < 8; ++u) reinterpret_cast<uint4*>(dst)[u] = make_uint4(0u, 0u, 0u, 0u);
+            for (int k = 0; k < 4; ++k) pos[k >> 1][k & 1] = pos_of(t, 64 * (k >> 1) + 16 * w4 + 8 * (k & 1) + sub);
+#pragma unroll 1
+            for (int j = 0; j < 4 && ok; ++j) {
+              Fp4Raw raw[2][2];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) raw[k >> 1][k & 1] = fp4_load(base, pos[k >> 1][k & 1], 4 * j + quad);
+#pragma unroll
+              for (int hf = 0; hf < 2; ++hf) {
+                if (hf == halves) break;
+                if (!(ok = acquire(mi.empty_v, it, kVStages))) break;
+                const uint32_t s = it % kVStages;
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                  const int r = 16 * w4 + 8 * k + sub;      // a missing token: codes and scales of zero
+                  fp4_store(sRingV + s * kStage + (second ? 8192 : 0) + r * 128, r, upper, second, raw[hf][k]);
+                }
+                fence_proxy_async_smem();
+                mbar_arrive(&mi.full_v[s]);
+                ++it;
               }
-              fence_proxy_async_smem();
-              mbar_arrive(&mi.full_v[s]);
-              ++it;
             }
           }
         }
@@ -702,9 +777,7 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
       named_bar_sync(bar_id, 128);
       low = __float_as_int(mi.red[4 * wg][0]);
       named_bar_sync(bar_id, 128);
-      float2 l[kCols / 2];
-#pragma unroll
-      for (int c = 0; c < kCols / 2; ++c) l[c] = make_float2(0.f, 0.f);
+      float l = 0.f;          // lane c: sum of row c0 + c over the warp's tokens
       const int32_t* const sel = p.k_sel >= 0 ? p.idx + static_cast<int64_t>(g.row0 / p.H) * p.k_sel : nullptr;
       const float4* const nm4 = reinterpret_cast<const float4*>(mi.nm + c0);
 
@@ -775,12 +848,9 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
             mi.f[c0 + wtid] = ex2_approx(old - now);
           }
           named_bar_sync(bar_id, 128);
+          scores();      // again: kept across the reduction they would not fit the registers
           shift();
-#pragma unroll
-          for (int c = 0; c < kCols / 2; ++c) {
-            l[c].x *= mi.f[c0 + 2 * c];
-            l[c].y *= mi.f[c0 + 2 * c + 1];
-          }
+          l *= mi.f[c0 + lane];
           if (t > 0) {
             // the sums so far, once every earlier product has landed in them
             ok = ok && __all_sync(0xffffffffu, mbar_wait(&mi.pv_done, (done - 1) & 1, wc));
@@ -809,9 +879,8 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
         if (nc > 0) {
 #pragma unroll
           for (int c = 0; c < kCols / 2; ++c) {
-            const float2 e = make_float2(ex2_approx(y[c].x), ex2_approx(y[c].y));
-            l[c] = __fadd2_rn(l[c], e);
-            pk[c] = FP4 ? pack_f16(e.x, e.y) : pack2(e.x, e.y);
+            y[c] = make_float2(ex2_approx(y[c].x), ex2_approx(y[c].y));
+            pk[c] = FP4 ? pack_f16(y[c].x, y[c].y) : pack2(y[c].x, y[c].y);
           }
         }
         // the weights' place in shared memory is free once the previous tile's product is done
@@ -827,16 +896,13 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
         }
         __syncwarp();
         if (lane == 0) mbar_arrive(&mi.p_full);
+        // the rows' sums over the warp's tokens (32 sums a thread instead did not fit the registers)
+        if (nc > 0) l += reduce_columns<false>(reinterpret_cast<float(&)[kCols]>(y), lane);
       }
       if (g.ntok > 0) ++segs;
-      // the rows' sums over the 128 threads
+      // the rows' sums over the warps
       named_bar_sync(bar_id, 128);
-      {
-        float v[kCols];
-#pragma unroll
-        for (int c = 0; c < kCols; ++c) v[c] = c & 1 ? l[c / 2].y : l[c / 2].x;
-        mi.red[warp - R::kFill][lane] = reduce_columns<false>(v, lane);
-      }
+      mi.red[warp - R::kFill][lane] = l;
       named_bar_sync(bar_id, 128);
       const bool whole = pc.first && pc.last;
       const int slot = 2 * blockIdx.x + (pc.first ? 1 : 0);     // head pieces 0, tail pieces 1
@@ -856,34 +922,9 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
         ok = ok && __all_sync(0xffffffffu, mbar_wait(&mi.pv_done, (done - 1) & 1, wc));
         tc_fence_after();
       }
-#pragma unroll 1
-      for (int u = 0; u < 4 * ((nc + 15) / 16); ++u) {
-        const int j = u & 3, cb = c0 + (u >> 2) * 16;         // block of dims, first of 16 rows
-        float o[16];
-        if (g.ntok > 0) tmem_ld16(tlane + j * kRows + cb, o);
-        const int dim = 128 * j + tok;
-        if (whole) {
-          // even lanes keep row c, odd lanes row c + 1, each with its pair of dims
-          __nv_bfloat16* ob = p.out + static_cast<int64_t>(g.row0 + cb + (lane & 1)) * kLatV + (dim & ~1);
-#pragma unroll
-          for (int c = 0; c < 16; c += 2) {
-            const float i0 = mi.f[cb + c], i1 = mi.f[cb + c + 1];
-            const float v0 = i0 != 0.f ? o[c] * i0 : 0.f, v1 = i1 != 0.f ? o[c + 1] * i1 : 0.f;
-            if (!FP4) {
-              if (v0 != v0 && i0 == i0) mi.spoiled[cb + c] = 1;
-              if (v1 != v1 && i1 == i1) mi.spoiled[cb + c + 1] = 1;
-            }
-            const float got = __shfl_xor_sync(0xffffffffu, lane & 1 ? v0 : v1, 1);
-            const uint32_t pr = lane & 1 ? pack2(got, v1) : pack2(v0, got);
-            if (cb + c + (lane & 1) < g.nrows) *reinterpret_cast<uint32_t*>(ob + c * kLatV) = pr;
-          }
-        } else {
-          float* const ob = w.o + slot * kSlotFloats + static_cast<int64_t>(cb) * kLatV + dim;
-#pragma unroll
-          for (int c = 0; c < 16; ++c)
-            if (cb + c < g.nrows) ob[c * kLatV] = o[c];
-        }
-      }
+      if (nc > 0)
+        write_sums<FP4>(p, mi.f, mi.spoiled, tlane, tok, c0, g.row0, g.nrows, g.ntok > 0,
+                        whole ? nullptr : w.o + slot * kSlotFloats);
       tc_fence_before();
       named_bar_sync(bar_id, 128);   // f, m and red are free for the next piece
       if (!FP4 && whole && wtid < nc && c0 + wtid < g.nrows && mi.spoiled[c0 + wtid])
