@@ -48,8 +48,8 @@ constexpr int kRows = 96;                    // rows (token, head) of a group
 constexpr int kTile = 128;                   // tokens of a tile
 constexpr int kQChunk = kRows * 128;         // 64 values of each row of Q
 constexpr int kQBytes = 9 * kQChunk;
-constexpr int kSStages = 3, kVStages = 2;    // stages of the two rings: scores, values
-constexpr int kStage = 16384;
+constexpr int kStage = 16384;                // 128 tokens x 64 values
+constexpr int kRings = 5 * kStage;           // both rings: scores, values
 constexpr int kPHalf = kTile * 128;          // weights of 64 rows: 128 tokens x 128 B
 constexpr int kCols = 32;                    // rows of the group a softmax thread holds
 constexpr int kSoftWarps = 12;
@@ -57,11 +57,16 @@ constexpr int kSoftWarps = 12;
 // Warps: fill, softmax (12), MMA (2 of 4).  A bf16 cache is filled by TMA from one thread a ring;
 // 4-bit rows are converted by four warps a ring.  Registers a thread at launch, then of each kind
 // of warp; the shares of the warpgroups add up to the launch's: 96 + 3 * 112 + 48 = 5 * 96 and
-// 2 * 64 + 3 * 104 + 40 = 6 * 80.
+// 2 * 72 + 3 * 96 + 48 = 6 * 80 (with 64 to fill and 104 for the softmax the fill spilled, and the
+// 4-bit decode batch of 32 took 734 us, not 593).
 template <bool FP4>
 struct Roles {
   static constexpr int kFill = FP4 ? 8 : 4, kMma = kFill + kSoftWarps, kThreads = (kMma + 4) * 32;
-  static constexpr int kFillRegs = FP4 ? 64 : 96, kSoftRegs = FP4 ? 104 : 112, kMmaRegs = FP4 ? 40 : 48;
+  static constexpr int kFillRegs = FP4 ? 72 : 96, kSoftRegs = FP4 ? 96 : 112, kMmaRegs = 48;
+  // Stages of the rings; a stage of values holds 128 dims of kVTok tokens.  4-bit rows fill two
+  // chunks of scores at a time, so that two such pairs make the ring, and values come by 32 tokens.
+  static constexpr int kS = FP4 ? 4 : 3, kV = 2, kVTok = FP4 ? 32 : 64, kVStage = kVTok * 256;
+  static_assert(kS * kStage + kV * kVStage <= kRings, "rings");
 };
 constexpr uint32_t kTmemS = 4 * kRows;       // O^T block j at 96 j, the scores behind them
 constexpr uint64_t kDrainNs = 200ull * 1000 * 1000;
@@ -339,8 +344,8 @@ __device__ __forceinline__ void fp4_store(uint8_t* row, int r, bool upper, bool 
 
 // ---------------------------------------------------------------- attention
 struct alignas(16) Misc {
-  uint64_t full_s[kSStages], empty_s[kSStages];
-  uint64_t full_v[kVStages], empty_v[kVStages], zero_req[kVStages], zeroed[kVStages];
+  uint64_t full_s[4], empty_s[4];
+  uint64_t full_v[2], empty_v[2], zero_req[2], zeroed[2];
   uint64_t q_full, q_empty, s_full, s_empty, p_full, pv_done, mma_done;
   uint32_t tmem;
   int abort;
@@ -355,8 +360,7 @@ struct alignas(16) Misc {
 };
 
 constexpr int kOffRing = kQBytes;
-constexpr int kOffRingV = kOffRing + kSStages * kStage;
-constexpr int kOffP = kOffRingV + kVStages * kStage;
+constexpr int kOffP = kOffRing + kRings;
 constexpr int kOffMisc = kOffP + 2 * kPHalf;
 constexpr int kSmem = kOffMisc + static_cast<int>(sizeof(Misc)) + 1024;
 static_assert(kSmem <= 232448, "shared memory per block");
@@ -438,24 +442,24 @@ template <bool FP4>
 __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
     latent_attention_kernel(const __grid_constant__ CUtensorMap tmQ, const __grid_constant__ CUtensorMap tmC,
                             const __grid_constant__ Params p) {
+  using R = Roles<FP4>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   uint8_t* const sQ = smem;
   uint8_t* const sRing = smem + kOffRing;
-  uint8_t* const sRingV = smem + kOffRingV;
+  uint8_t* const sRingV = sRing + Roles<FP4>::kS * kStage;
   uint8_t* const sP = smem + kOffP;
   Misc& mi = *reinterpret_cast<Misc*>(smem + kOffMisc);
 
-  using R = Roles<FP4>;
   constexpr int kMmaWarp = R::kMma;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const Ws& w = p.ws;
   if (threadIdx.x == 0) {
-    for (int s = 0; s < kSStages; ++s) {
+    for (int s = 0; s < R::kS; ++s) {
       mbar_init(&mi.full_s[s], FP4 ? 128 : 1);
       mbar_init(&mi.empty_s[s], 1);
     }
-    for (int s = 0; s < kVStages; ++s) {
+    for (int s = 0; s < R::kV; ++s) {
       mbar_init(&mi.full_v[s], FP4 ? 128 : 1);
       mbar_init(&mi.empty_v[s], 1);
       mbar_init(&mi.zero_req[s], 1);
@@ -589,8 +593,8 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
 #pragma unroll
                 for (int k = 0; k < 4; ++k) nx[k] = fp4_load(base, pos[k], 4 * (c + 1) + quad);
               }
-              const uint32_t s0 = it % kSStages, s1 = (it + 1) % kSStages;
-              if (!(ok = __all_sync(0xffffffffu, acquire(mi.empty_s, it, kSStages) && acquire(mi.empty_s, it + 1, kSStages)))) break;
+              const uint32_t s0 = it % R::kS, s1 = (it + 1) % R::kS;
+              if (!(ok = __all_sync(0xffffffffu, acquire(mi.empty_s, it, R::kS) && acquire(mi.empty_s, it + 1, R::kS)))) break;
               uint8_t* const dst = sRing + (second ? s1 : s0) * kStage;
 #pragma unroll
               for (int k = 0; k < 4; ++k) {
@@ -613,8 +617,8 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
               v[k] = a >= 0 ? *reinterpret_cast<const uint4*>(base + static_cast<int64_t>(a) * kLatRow4 + kLatCodes + kLatScales + 16 * (lane & 7))
                             : make_uint4(0u, 0u, 0u, 0u);
             }
-            const uint32_t s = it % kSStages;
-            if (!(ok = __all_sync(0xffffffffu, acquire(mi.empty_s, it, kSStages)))) break;
+            const uint32_t s = it % R::kS;
+            if (!(ok = __all_sync(0xffffffffu, acquire(mi.empty_s, it, R::kS)))) break;
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
               const int r = 32 * w4 + 4 * k + (lane >> 3);
@@ -626,26 +630,23 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
           }
         } else {
           for (int t = pc.t0; t < pc.t0 + pc.n && ok; ++t) {
-            const int halves = tile_tokens(pc.g, t) > 64 ? 2 : 1;
-            // the warp's 16 rows of either half
-            int pos[2][2];
+            const int parts = (tile_tokens(pc.g, t) + R::kVTok - 1) / R::kVTok;
+            // the warp's eight rows of each 32
+            int pos[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) pos[k >> 1][k & 1] = pos_of(t, 64 * (k >> 1) + 16 * w4 + 8 * (k & 1) + sub);
+            for (int k = 0; k < 4; ++k) pos[k] = pos_of(t, 32 * k + 8 * w4 + sub);
 #pragma unroll 1
             for (int j = 0; j < 4 && ok; ++j) {
-              Fp4Raw raw[2][2];
+              Fp4Raw raw[4];
 #pragma unroll
-              for (int k = 0; k < 4; ++k) raw[k >> 1][k & 1] = fp4_load(base, pos[k >> 1][k & 1], 4 * j + quad);
+              for (int k = 0; k < 4; ++k) raw[k] = fp4_load(base, pos[k], 4 * j + quad);
 #pragma unroll
-              for (int hf = 0; hf < 2; ++hf) {
-                if (hf == halves) break;
-                if (!(ok = acquire(mi.empty_v, it, kVStages))) break;
-                const uint32_t s = it % kVStages;
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                  const int r = 16 * w4 + 8 * k + sub;      // a missing token: codes and scales of zero
-                  fp4_store(sRingV + s * kStage + (second ? 8192 : 0) + r * 128, r, upper, second, raw[hf][k]);
-                }
+              for (int k = 0; k < 4; ++k) {
+                if (k == parts) break;
+                if (!(ok = acquire(mi.empty_v, it, R::kV))) break;
+                const uint32_t s = it % R::kV;
+                const int r = 8 * w4 + sub;                 // a missing token: codes and scales of zero
+                fp4_store(sRingV + s * R::kVStage + (second ? R::kVStage / 2 : 0) + r * 128, r, upper, second, raw[k]);
                 fence_proxy_async_smem();
                 mbar_arrive(&mi.full_v[s]);
                 ++it;
@@ -666,8 +667,8 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
           const bool two = tile_tokens(pc.g, t) > 64;
           const int y = static_cast<int>(pc.g.kv_row0) + t * kTile;
           for (int c = 0; c < 9; ++c) {
-            if (!(ok = acquire(mi.empty_s, it, kSStages))) break;
-            const uint32_t s = it % kSStages;
+            if (!(ok = acquire(mi.empty_s, it, R::kS))) break;
+            const uint32_t s = it % R::kS;
             mbar_arrive_expect_tx(&mi.full_s[s], two ? kStage : kStage / 2);
             const uint64_t pol = c < 8 ? keep : drop;
             tma_load_2d_hint(sRing + s * kStage, &tmC, &mi.full_s[s], 64 * c, y, pol);
@@ -677,8 +678,8 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
         }
       }
       if (!ok) {
-        for (uint32_t k = it > kSStages ? it - kSStages : 0; k < it; ++k)
-          drain(&mi.full_s[k % kSStages], (k / kSStages) & 1);
+        for (uint32_t k = it > R::kS ? it - R::kS : 0; k < it; ++k)
+          drain(&mi.full_s[k % R::kS], (k / R::kS) & 1);
         if (segs > 0) drain(&mi.q_full, (segs - 1) & 1);
       }
     } else if (warp == 1 && lane == 0) {
@@ -690,19 +691,19 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
           for (int k = 0; k < 4 * halves; ++k) {
             const int j = halves == 2 ? k >> 1 : k, hf = halves == 2 ? k & 1 : 0;
             const int y = static_cast<int>(pc.g.kv_row0) + t * kTile + 64 * hf;
-            if (!(ok = acquire(mi.empty_v, it, kVStages))) break;
-            const uint32_t s = it % kVStages;
+            if (!(ok = acquire(mi.empty_v, it, R::kV))) break;
+            const uint32_t s = it % R::kV;
             mbar_arrive_expect_tx(&mi.full_v[s], kStage);
-            tma_load_2d_hint(sRingV + s * kStage, &tmC, &mi.full_v[s], 128 * j, y, drop);
-            tma_load_2d_hint(sRingV + s * kStage + kStage / 2, &tmC, &mi.full_v[s], 128 * j + 64, y, drop);
+            tma_load_2d_hint(sRingV + s * R::kVStage, &tmC, &mi.full_v[s], 128 * j, y, drop);
+            tma_load_2d_hint(sRingV + s * R::kVStage + kStage / 2, &tmC, &mi.full_v[s], 128 * j + 64, y, drop);
             if (hf == halves - 1 && (v & 15)) mbar_arrive(&mi.zero_req[s]);
             ++it;
           }
         }
       }
       if (!ok)
-        for (uint32_t k = it > kVStages ? it - kVStages : 0; k < it; ++k)
-          drain(&mi.full_v[k % kVStages], (k / kVStages) & 1);
+        for (uint32_t k = it > R::kV ? it - R::kV : 0; k < it; ++k)
+          drain(&mi.full_v[k % R::kV], (k / R::kV) & 1);
     } else if (warp == 2) {
       // zero the rows of a group's last tile that its MMAs read behind its last token
       uint32_t ph = 0;      // per-stage phase bits of zero_req
@@ -715,8 +716,8 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
           const int halves = v > 64 ? 2 : 1;
           const int r0 = v - 64 * (halves - 1), r1 = (r0 + 15) & ~15;
           for (int j = 0; j < 4 && ok; ++j) {
-            const uint32_t at = it + stages - 4 * halves + j * halves + (halves - 1), s = at % kVStages;
-            ok = mbar_wait(&mi.zero_req[s], (ph >> s) & 1, wc) && mbar_wait(&mi.full_v[s], (at / kVStages) & 1, wc);
+            const uint32_t at = it + stages - 4 * halves + j * halves + (halves - 1), s = at % R::kV;
+            ok = mbar_wait(&mi.zero_req[s], (ph >> s) & 1, wc) && mbar_wait(&mi.full_v[s], (at / R::kV) & 1, wc);
             if (!__all_sync(0xffffffffu, ok)) {
               ok = false;
               break;
@@ -724,7 +725,7 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
             ph ^= 1u << s;
             for (int u = lane; u < (r1 - r0) * 16; u += 32) {
               const int r = r0 + (u >> 4), un = u & 15;
-              *reinterpret_cast<uint4*>(sRingV + s * kStage + (un >> 3) * 8192 + r * 128 + (un & 7) * 16) =
+              *reinterpret_cast<uint4*>(sRingV + s * R::kVStage + (un >> 3) * 8192 + r * 128 + (un & 7) * 16) =
                   make_uint4(0u, 0u, 0u, 0u);
             }
             fence_proxy_async_smem();
@@ -945,7 +946,7 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
       };
       uint32_t nth = 0;       // tiles so far
       if (warp == kMmaWarp) {
-        Ring<kSStages> rg;
+        Ring<R::kS> rg;
         uint32_t segs = 0;
         const uint32_t q_lo = desc_lo(smem_u32(sQ), 16), r_lo = desc_lo(smem_u32(sRing), 16);   // K-major
         while (ok && walk.next(&pc)) {
@@ -973,37 +974,38 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
           }
         }
       } else {
-        Ring<kVStages> rg;
+        Ring<R::kV> rg;
         uint32_t zph = 0;
-        const uint32_t v_lo = desc_lo(smem_u32(sRingV), 8192), p_lo = desc_lo(smem_u32(sP), kPHalf);   // MN-major
+        const uint32_t v_lo = desc_lo(smem_u32(sRingV), R::kVStage / 2), p_lo = desc_lo(smem_u32(sP), kPHalf);   // MN-major
         while (ok && walk.next(&pc)) {
           const Group& g = pc.g;
           if (g.ntok == 0) continue;
           const int n16 = (g.nrows + 15) / 16 * 16;
           const uint32_t idesc = (FP4 ? idesc_f16(128, n16) : umma_idesc_bf16(128, n16)) | (1u << 15) | (1u << 16);
           for (int t = 0; t < pc.n && ok; ++t, ++nth) {
-            const int v = tile_tokens(g, pc.t0 + t), halves = v > 64 ? 2 : 1;
+            const int v = tile_tokens(g, pc.t0 + t), parts = (v + R::kVTok - 1) / R::kVTok;
             const bool zero = !FP4 && pc.last && t == pc.n - 1 && (v & 15);
             if (!(ok = wait(&mi.p_full, nth & 1))) break;
             tc_fence_after();
 #pragma unroll 1
             for (int j = 0; j < 4 && ok; ++j) {
 #pragma unroll 1
-              for (int hf = 0; hf < halves; ++hf) {
-                if (zero && hf == halves - 1) {
+              for (int part = 0; part < parts; ++part) {
+                if (zero && part == parts - 1) {
                   if (!(ok = wait(&mi.zeroed[rg.s], (zph >> rg.s) & 1))) break;
                   zph ^= 1u << rg.s;
                 }
                 if (!(ok = wait(&mi.full_v[rg.s], rg.phase))) break;
                 tc_fence_after();
-                const int left = v - 64 * hf;
-                const uint32_t a = v_lo + rg.s * (kStage >> 4), b = p_lo + hf * (8192 >> 4), d = tmem + j * kRows;
-                if (left >= 64) {
+                const int left = v - R::kVTok * part;
+                const uint32_t a = v_lo + rg.s * (R::kVStage >> 4), b = p_lo + part * (R::kVTok * 128 >> 4), d = tmem + j * kRows;
+                if (left >= R::kVTok) {
 #pragma unroll
-                  for (int k = 0; k < 4; ++k) umma_lo(d, a + k * 128, b + k * 128, idesc, (t | hf | k) != 0, leader);
+                  for (int k = 0; k < R::kVTok / 16; ++k)
+                    umma_lo(d, a + k * 128, b + k * 128, idesc, (t | part | k) != 0, leader);
                 } else {
                   for (int k = 0; k < (left + 15) / 16; ++k)
-                    umma_lo(d, a + k * 128, b + k * 128, idesc, (t | hf | k) != 0, leader);
+                    umma_lo(d, a + k * 128, b + k * 128, idesc, (t | part | k) != 0, leader);
                 }
                 commit(&mi.empty_v[rg.s]);
                 rg.next();
