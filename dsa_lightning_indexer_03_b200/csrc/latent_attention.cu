@@ -12,21 +12,22 @@
 // and O^T += C_latent^T . P^T (M = 4 x 128 latent dims, N = rows, K = 128 tokens).  So M is
 // always full (96 rows as M would waste a quarter of it), the whole 512-dim output of a group
 // (4 x 96 fp32 columns) and its scores (96) fit in one SM's TMEM, and the scores of a tile are
-// computed once.  Q (96 x 576, 108 KB) stays in shared memory; the cache streams through a ring
-// of 16 KB stages: nine 64-value chunks of a tile for its scores, then the tile again (from L2)
-// as eight 64-token x 128-dim pieces for its values, since Q and a whole 144 KB tile do not fit
-// together.
+// computed once.  Q (96 x 576, 108 KB) stays in shared memory; the cache streams through two
+// rings: nine 64-value chunks of a tile for its scores, then the tile again (from L2) as pieces of
+// 64 tokens x 128 dims for its values, since Q and a whole 144 KB tile do not fit together.
 //
-// latent_attention_kernel: persistent, one block of 20 warps per SM.
-//   warps 0-3   fill the ring: one thread with TMA (bf16), or all by converting 4-bit rows; for
-//               bf16 warp 2 zeroes the rows behind a sequence's last token (0 * NaN is NaN).
-//   warps 4-15  softmax: a thread per token, a third of the rows each.  The reference m of a row
-//               is its running maximum, raised only when a score exceeds it by more than 8 (log2
-//               units, so weights stay below 256): most tiles then need no maximum over the
-//               tokens, which lie across threads, only a vote.  Sums are taken over the warp
-//               in every tile, over the warps at the end.  Weights go to shared memory as bf16 (the MMA's operand).
-//   warp 16     (of a warpgroup that otherwise idles) issues the MMAs: S(t+1) before the values of t, so that the softmax of a tile
-//               runs under the MMAs of its neighbours.
+// latent_attention_kernel: persistent, one block of 20 (bf16) or 24 (4-bit) warps per SM.
+//   fill      bf16: one thread a ring, with TMA, and a warp that zeroes the rows behind a
+//             sequence's last token (0 * NaN is NaN).  4-bit: four warps a ring convert the rows,
+//             to fp16, in which their values are exact; queries then are scaled by powers of two
+//             into fp16 too (their rope part, and the rope keys, stay bf16: an MMA of their own).
+//   softmax   12 warps, a thread per token and a third of the rows.  The reference m of a row is
+//             its running maximum, raised only when a score exceeds it by more than 8 (log2 units,
+//             so weights stay below 256): most tiles then need no maximum over the tokens, which
+//             lie across threads, only a vote.  Sums are taken over the warp in every tile, over
+//             the warps at the end.  Weights go to shared memory in the values' type.
+//   MMA       two warps, one for the scores and one for the values, so that the scores of the
+//             next tile run beside the values of this one, and the softmax under both.
 // Work: plan_kernel lists the groups and their tiles; the blocks take equal shares of all tiles
 // in order, so a share may begin or end inside a group; such pieces leave unnormalised fp32
 // sums and (m, l) in the workspace, which merge_kernel joins in a fixed order.
@@ -35,8 +36,11 @@
 // weight for the others is 0, and 0 * NaN spoils their sums.  Such rows of out (NaN under a
 // finite sum of weights) are listed and computed again by merge_kernel over their own prefix.
 //
-// Bound: 1,152 B (bf16) and 2 * 96 * 1,088 flop a cached token at 96 rows; on chip, 765 KB
-// of shared-memory traffic a tile (operands of both products and the ring's writes).
+// Bound: 1,152 B (bf16) and 2 * 96 * 1,088 flop a cached token at 96 rows.  Measured: 7,400
+// cycles a tile where the cache lies in L2 (a prompt chunk; the MMAs alone 3,260, the 765 KB of
+// shared-memory traffic of both products' operands and the rings 6,000), 8,900 where it comes from
+// memory (5,800 at the copy rate; a third of the rows is read twice all the same).  4-bit rows
+// take 15,000: the conversion of a tile, once for each product, and the waits between its steps.
 
 #include "latent.h"
 #include "latent_mma.cuh"
@@ -552,7 +556,7 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
 #pragma unroll
             for (int c = 0; c < 9; ++c) top = __vmaxu2(top, v[c] & 0x7FFF7FFFu);
             top = __reduce_max_sync(0xffffffffu, top >> 16 > (top & 0xFFFFu) ? top >> 16 : top & 0xFFFFu);
-            const int f = scale_exponent(__uint_as_float(top << 16));
+            const int f = scale_exponent(__uint_as_float(top << 16), kLowestFactor);
             const float inv = pow2(-f);
 #pragma unroll
             for (int c = 0; c < 9; ++c) {

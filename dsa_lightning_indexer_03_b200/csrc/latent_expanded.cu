@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(kUpThreads, 1)
       named_bar_sync(1 + part, 128);
       top = fmaxf(fmaxf(mi.red[4 * part], mi.red[4 * part + 1]), fmaxf(mi.red[4 * part + 2], mi.red[4 * part + 3]));
       named_bar_sync(1 + part, 128);
-      const int f = scale_exponent(top);
+      const int f = scale_exponent(top, part == 0 ? kLowestFactor : kLowestValue);
       const float inv = pow2(-f);
       uint8_t* const dst = w.kv + (tile * H + h) * kKvBytes + part * 3 * kChunk + r * 128;
 #pragma unroll 1
@@ -825,7 +825,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
           // magnitudes of bf16 pairs compare as integers (a row with an infinity is lost anyway)
           uint32_t top = __vmaxu2(__vmaxu2(v[k][0] & 0x7FFF7FFFu, v[k][1] & 0x7FFF7FFFu), v[k][2] & 0x7FFF7FFFu);
           top = __reduce_max_sync(0xffffffffu, top >> 16 > (top & 0xFFFFu) ? top >> 16 : top & 0xFFFFu);
-          const int f = scale_exponent(__uint_as_float(top << 16));
+          const int f = scale_exponent(__uint_as_float(top << 16), kLowestFactor);
           const float inv = pow2(-f);
 #pragma unroll
           for (int c = 0; c < 3; ++c)

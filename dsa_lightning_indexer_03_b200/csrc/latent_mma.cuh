@@ -133,11 +133,15 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
 // 2^e, e in [-126, 127]
 __device__ __forceinline__ float pow2(int e) { return __uint_as_float(static_cast<uint32_t>(e + 127) << 23); }
 
-// Exponent f of the scale 2^f that brings a largest magnitude of `top` to below 2^15, so that
-// fp16 holds it; nothing is lifted by more than 2^14.
-__device__ __forceinline__ int scale_exponent(float top) {
+// Exponent f of the scale 2^f that brings a largest magnitude of `top` to between 2^14 and 2^15,
+// where fp16 holds it and what lies up to 2^28 below it in full; magnitudes below 2^lowest are
+// lifted no further.
+__device__ __forceinline__ int scale_exponent(float top, int lowest) {
   const int e = static_cast<int>((__float_as_uint(top) >> 23) & 0xFF) - 127;
-  return (e < 0 ? 0 : e) - 14;
+  return (e < lowest ? lowest : e) - 14;
 }
+// Of queries and keys: a factor of a score, down to where its product stays normal.  Of values: the
+// weights take the scale over, so those of one row's tiles must stay within fp32 of each other.
+constexpr int kLowestFactor = -106, kLowestValue = -60;
 
 }  // namespace dsa

@@ -303,11 +303,11 @@ dsa_status_t dsa_indexer_sparse_mla(dsa_indexer_t h, int64_t T, const void* q, i
  *                 may overlap on the GPU need a workspace each
  * A position outside [-1, rows of the sequence) gives out = 0 and lse = -inf and sets
  * DSA_ERR_DEVICE_BOUNDS; malformed offsets set it too and give every query of the call out = 0
- * and lse = -inf.  Cache rows past a sequence's largest queried position are never used,
- * whatever they hold; a row that one of a sequence's queries attends to must hold finite
- * values for the sequence's other queries to be defined.  Scores, softmax statistics and
- * outputs are accumulated in fp32; the weights multiply the values as bf16, and out is rounded
- * to bf16 once.  T = 0 is a no-op; asynchronous on `stream`. */
+ * and lse = -inf.  Cache rows that a query does not attend to are never used for it, whatever
+ * they hold (a NaN beside a query's prefix costs it a second, slow pass).  Scores, softmax
+ * statistics and outputs are accumulated in fp32; the weights multiply the values as bf16 (a bf16
+ * cache) or fp16 (a 4-bit cache, the expanded form), and out is rounded to bf16 once.  T = 0 is a
+ * no-op; asynchronous on `stream`. */
 
 /* Bytes of workspace that dsa_indexer_latent_attention and _latent_attention_fp4 need for T
  * tokens of n_heads heads in B sequences (-1 for a bad argument). */
@@ -361,12 +361,14 @@ int64_t dsa_indexer_latent_expanded_workspace(dsa_indexer_t h, int64_t T, int32_
  *   q     bf16 [T, n_heads, 192] (128 values without a rotary step, then 64 rope values)
  *   kv_cache bf16 [cache_rows, 576], W_ukv bf16 [n_heads, 256, 512] (a head's 128 key rows, then
  *         its 128 value rows; out x in)
- *   k[s,h] = bf16(W_ukv[h][0..127] kv[s][0..511]) | kv[s][512..575],
- *   v[s,h] = bf16(W_ukv[h][128..255] kv[s][0..511]),
+ *   k[s,h] = W_ukv[h][0..127] kv[s][0..511] | kv[s][512..575],
+ *   v[s,h] = W_ukv[h][128..255] kv[s][0..511],
  *   out[t,h] = sum_s softmax_s(scale * (q[t,h] . k[s,h])) v[s,h],  bf16 [T, n_heads, 128]
- * Every one of the cache_rows rows is expanded: pass the part of the cache that holds the
- * call's sequences, with cache_offsets counted from its first row (at most 8,388,480 rows;
- * more: DSA_ERR_UNSUPPORTED). */
+ * Keys and values are fp32 sums kept in fp16, each 128 tokens of a head under scales of their own
+ * (powers of two); values of a row's tokens may differ by up to 2^100 in magnitude between those.
+ * Only rows that some query attends to are expanded, but the workspace is sized for cache_rows:
+ * pass the part of the cache that holds the call's sequences, with cache_offsets counted from
+ * its first row (at most 8,388,480 rows; more: DSA_ERR_UNSUPPORTED). */
 dsa_status_t dsa_indexer_latent_attention_expanded(dsa_indexer_t h, int64_t T, const void* q, int32_t n_heads,
                                                    const void* kv_cache, int64_t cache_rows, const void* W_ukv,
                                                    const int32_t* positions, const int32_t* q_seq_offsets, int32_t B,
