@@ -571,6 +571,10 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
           ++segs;
           auto prefetch = [&](int t) {
             if (t >= pc.t0 + pc.n) return;
+            if (!sel) {            // rows follow one another: one instruction for all
+              if (threadIdx.x == 0) prefetch_l2(base + static_cast<int64_t>(t) * kTile * kLatRow4, tile_tokens(pc.g, t) * kLatRow4);
+              return;
+            }
             const int pos = pos_of(t, threadIdx.x & 127);
             if (pos < 0) return;
             const uint8_t* const r = base + static_cast<int64_t>(pos) * kLatRow4;
@@ -1036,9 +1040,9 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
 }
 
 // ---------------------------------------------------------------- merge
-// Rows of the groups that several blocks share, from the pieces in the order of their tiles, a
-// block of threads a row at a time; with malformed offsets, rows of the call as attending to nothing.
-constexpr int kMergeThreads = 128;
+// Rows of the groups that several blocks share, from the pieces in the order of their tiles, four
+// rows a block at a time, so that their loads are in flight together; with malformed offsets, rows of the call as attending to nothing.
+constexpr int kMergeThreads = 128, kMergeRows = 4;
 
 // Row `row` of out from its own prefix alone, by the block: scores of 128 tokens at a time, a
 // thread each, then four of the 512 dims a thread.  For rows that a NaN or an infinity beside
@@ -1102,46 +1106,53 @@ __global__ void __launch_bounds__(kMergeThreads) latent_merge_kernel(Params p, i
     return;
   }
   for (int k = blockIdx.x; k < plan.spoiled; k += gridDim.x) redo_row(p, w.spoiled[k]);
-  for (int item = blockIdx.x; item < plan.merges * kRows; item += gridDim.x) {
-    const Merge mg = w.merge[item / kRows];
-    const int r = item % kRows;
-    if (r >= mg.nrows) continue;
-    // pieces: the tail slot of the first block, then the head slots of the others (a block with an
-    // empty share, where there are fewer tiles than blocks, has none)
-    float m = kUnset;
+  for (int item = blockIdx.x; item < plan.merges * (kRows / kMergeRows); item += gridDim.x) {
+    const Merge mg = w.merge[item / (kRows / kMergeRows)];
+    const int r0 = item % (kRows / kMergeRows) * kMergeRows;
+    if (r0 >= mg.nrows) continue;
+    // pieces: the tail slot of the first block, then the head slots of the others
+    float m[kMergeRows], l[kMergeRows];
+    float4 o[kMergeRows];
+#pragma unroll
+    for (int r = 0; r < kMergeRows; ++r) m[r] = kUnset, l[r] = 0.f, o[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
     for (int k = mg.first; k <= mg.last; ++k) {
-      int64_t x, y;
-      share(plan.tiles, k, blocks, &x, &y);
-      if (x >= y) continue;
-      const float2 v = w.ml[static_cast<int64_t>(2 * k + (k == mg.first)) * kRows + r];
-      if (v.y != 0.f) m = fmaxf(m, v.x);
-    }
-    float l = 0.f;
-    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int k = mg.first; k <= mg.last; ++k) {
-      int64_t x, y;
-      share(plan.tiles, k, blocks, &x, &y);
-      if (x >= y) continue;
-      const int64_t slot = 2 * k + (k == mg.first);
-      const float2 v = w.ml[slot * kRows + r];
-      const float4 c = reinterpret_cast<const float4*>(w.o + slot * kSlotFloats + static_cast<int64_t>(r) * kLatV)[tid];
-      if (v.y != 0.f) {
-        const float f = ex2_approx(v.x - m);
-        l = fmaf(v.y, f, l);
-        o.x = fmaf(c.x, f, o.x);
-        o.y = fmaf(c.y, f, o.y);
-        o.z = fmaf(c.z, f, o.z);
-        o.w = fmaf(c.w, f, o.w);
+      if (plan.tiles < blocks) {      // with fewer tiles than blocks some shares are empty
+        int64_t x, y;
+        share(plan.tiles, k, blocks, &x, &y);
+        if (x >= y) continue;
+      }
+      const int64_t at = static_cast<int64_t>(2 * k + (k == mg.first)) * kRows + r0;
+      float2 v[kMergeRows];
+      float4 c[kMergeRows];
+#pragma unroll
+      for (int r = 0; r < kMergeRows; ++r) {
+        v[r] = w.ml[at + r];
+        c[r] = reinterpret_cast<const float4*>(w.o + (at + r) * kLatV)[tid];
+      }
+#pragma unroll
+      for (int r = 0; r < kMergeRows; ++r) {
+        if (v[r].y == 0.f) continue;          // no token of the row in this piece
+        const float now = fmaxf(m[r], v[r].x), f0 = ex2_approx(m[r] - now), f1 = ex2_approx(v[r].x - now);
+        m[r] = now;
+        l[r] = fmaf(l[r], f0, v[r].y * f1);
+        o[r].x = fmaf(o[r].x, f0, c[r].x * f1);
+        o[r].y = fmaf(o[r].y, f0, c[r].y * f1);
+        o[r].z = fmaf(o[r].z, f0, c[r].z * f1);
+        o[r].w = fmaf(o[r].w, f0, c[r].w * f1);
       }
     }
-    const float inv = l != 0.f ? 1.f / l : 0.f;
-    const int64_t row = mg.row0 + r;
-    reinterpret_cast<uint2*>(p.out + row * kLatV)[tid] =
-        l != 0.f ? make_uint2(pack2(o.x * inv, o.y * inv), pack2(o.z * inv, o.w * inv)) : make_uint2(0u, 0u);
-    if (tid == 0) p.lse[row] = l != 0.f ? fmaf(m, 0.69314718055994531f, logf(l)) : -INFINITY;
-    const bool nan = l == l && l != 0.f && !(o.x == o.x && o.y == o.y && o.z == o.z && o.w == o.w);
-    if (p.kv && __syncthreads_or(nan)) redo_row(p, row);
+#pragma unroll
+    for (int r = 0; r < kMergeRows; ++r) {
+      if (r0 + r >= mg.nrows) break;
+      const float inv = l[r] != 0.f ? 1.f / l[r] : 0.f;
+      const int64_t row = mg.row0 + r0 + r;
+      reinterpret_cast<uint2*>(p.out + row * kLatV)[tid] =
+          l[r] != 0.f ? make_uint2(pack2(o[r].x * inv, o[r].y * inv), pack2(o[r].z * inv, o[r].w * inv)) : make_uint2(0u, 0u);
+      if (tid == 0) p.lse[row] = l[r] != 0.f ? fmaf(m[r], 0.69314718055994531f, logf(l[r])) : -INFINITY;
+      const bool nan = l[r] == l[r] && l[r] != 0.f && !(o[r].x == o[r].x && o[r].y == o[r].y && o[r].z == o[r].z && o[r].w == o[r].w);
+      if (p.kv && __syncthreads_or(nan)) redo_row(p, row);
+    }
   }
 }
 

@@ -73,6 +73,11 @@ __device__ __forceinline__ void umma_lo(uint32_t d, uint32_t a_lo, uint32_t b_lo
       : "memory");
 }
 
+// fetch of `bytes` (a multiple of 16) from a 16-byte aligned address into L2
+__device__ __forceinline__ void prefetch_l2(const void* p, uint32_t bytes) {
+  asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(p), "r"(bytes) : "memory");
+}
+
 // position in a ring of N stages and the parity of its full barriers
 template <int N>
 struct Ring {
