@@ -24,8 +24,8 @@
 //   weights replace the scores in TMEM (the A operand of the second product).  K and V of 128 tokens
 //   are 80 KB, read once for both tiles, through rings of four 16 KB and two 32 KB stages.
 //   Items are taken in order from a counter, longest first among a sequence's; the heads go in
-//   groups whose keys and values fit L2.  When there are too few items for that to balance,
-//   every block takes an equal share of all 128-token steps instead, and merge_expanded_kernel
+//   groups whose keys and values fit L2.  When there are too few long items for that to
+//   balance, every block takes an equal share of all 128-token steps instead, and merge_expanded_kernel
 //   joins the pieces of an item.
 //
 // Bound: the tensor core, 128 x 128 x (192 + 128) products in 1,280 cycles, and close behind
@@ -1081,8 +1081,13 @@ cudaError_t launch_latent_expanded(const ExpandedArgs& a, const CUtensorMap& tmC
   p.ws = carve(a.workspace, a.T, a.B, a.H, a.cache_rows, blocks);
   p.err = a.err;
   p.timeout_ns = a.timeout_ns;
-  // fewer than six items a block would leave blocks idle at the end
-  p.split = (static_cast<int64_t>(a.T) + kPair - 1) / kPair * a.H < 6 * blocks;
+  // Whole items leave blocks idle in their last round; equal shares cost two more starts a block and
+  // the merge, about as much as 12 steps.  Measured, items / shares: 2,000 tokens x 24 heads 83 / 116
+  // us, ragged 3,802 x 32 130 / 177; 1,500 tokens after 6,500 x 32 heads 330 / 301, 1,000 after
+  // 11,000 x 24 295 / 259.  From four items a block on the counter evens them out by itself.
+  const int64_t items = (static_cast<int64_t>(a.T) + kPair - 1) / kPair * a.H;
+  const int64_t idle = (blocks - items % blocks) % blocks, steps = a.cache_rows / (static_cast<int64_t>(a.B) * kTok) + 1;
+  p.split = items < 4 * blocks && idle * steps > 12 * blocks;
   cudaError_t e = cudaFuncSetAttribute(up_project_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kUpSmem);
   if (e == cudaSuccess) e = cudaFuncSetAttribute(expanded_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
   if (e != cudaSuccess) return e;

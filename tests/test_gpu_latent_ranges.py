@@ -194,3 +194,50 @@ def test_4bit_error_is_that_of_fp16_weights(dsa, ix):
     tol = 1.01 * U * np.abs(ref) + (1.05 * F + 2 * np.expm1(e)[..., None]) * (mag + np.abs(ref)) + 2.0 ** -19 * np.abs(val).max()
     assert np.all(np.abs(o - ref) <= tol)
     assert np.all(np.abs(lse - lref) <= e + 2.0 ** -22 * (np.abs(lref) + 8) + 1e-6)
+
+
+@pytest.mark.parametrize("lens,nq,H", [([2500], [300], 3), ([1900, 1700], [1, 260], 5), ([5000], [5], 2),
+                                       ([3000], [129], 1)])
+def test_expanded_few_long_items_in_equal_shares(dsa, ix, lens, nq, H):
+    b, w = Batch(80 + H, lens, nq, H, dim=192), _weights(30 + H, H)
+    o = _expanded(ix, b, w)
+    assert ix.device_error() == dsa.DSA_OK
+    _check_exact(o, b, w)
+    assert np.array_equal(o, _expanded(ix, b, w))
+
+
+def test_expanded_equal_shares_beside_a_nan_and_without_tokens(dsa, ix):
+    b, w = Batch(81, [2200], [400], 3, dim=192), _weights(31, 3)
+    b.kv[2000, 11] = float("nan")
+    b.pos[7], b.pos[8] = -1, 3
+    o = _expanded(ix, b, w)
+    assert ix.device_error() == dsa.DSA_OK
+    assert np.all(o[7] == 0) and not np.any(np.isfinite(o[200:]).all(axis=2))
+    b.kv = torch.nan_to_num(b.kv, 0)
+    _check_exact(o, b, w, tokens={0, 5, 7, 8, 100, 199})
+    b.co = torch.tensor([0, 2201], dtype=torch.int64)
+    assert np.all(_expanded(ix, b, w) == 0) and ix.device_error() == dsa.DSA_ERR_DEVICE_BOUNDS
+
+
+def test_prompt_then_decode_through_one_cache(dsa, ix):
+    # a prompt in the expanded form, its latents into the 4-bit cache, then tokens in the absorbed
+    # form over both caches: the absorbed form over the values the 4-bit rows stand for is the same
+    # operator over another cache, so its two results differ by the weights' types alone
+    H, n = 16, 700
+    b, w = Batch(82, [n], [n], H, dim=192), _weights(32, H)
+    _check_exact(_expanded(ix, b, w), b, w, tokens=set(range(0, n, 37)))
+    kv = b.kv.to(DEV)
+    cache4 = torch.zeros((n + 3, 416), dtype=torch.uint8, device=DEV)
+    ix.quantize_latent_fp4(kv, out=cache4, rows=torch.arange(3, n + 3, device=DEV))
+    back = ix.dequantize_latent_fp4(cache4, rows=torch.arange(3, n + 3, device=DEV))
+    d = Batch(83, [n], [4], H)
+    q, pos = d.q.to(DEV), d.pos.to(DEV)
+    qo = torch.tensor([0, 4], dtype=torch.int32, device=DEV)
+    co4 = torch.tensor([3, n + 3], dtype=torch.int64, device=DEV)
+    co = torch.tensor([0, n], dtype=torch.int64, device=DEV)
+    o4, l4 = (f64(x) for x in ix.latent_attention_fp4(q, cache4, pos, qo, co4, SCALE))
+    o, lse = (f64(x) for x in ix.latent_attention(q, back, pos, qo, co, SCALE))
+    assert ix.device_error() == dsa.DSA_OK
+    ref, lref, mag = oracle.latent_attention(f64(d.q), f64(back), d.pos.numpy(), [0, 4], [0, n], SCALE)
+    assert np.all(np.abs(o4 - o) <= 2.02 * U * np.abs(ref) + (1.01 * U + 1.1 * F + 1e-4) * (mag + np.abs(ref)) + 1e-5)
+    assert np.all(np.abs(l4 - lse) <= 1e-4) and np.all(np.abs(lse - lref) <= 1e-4)
