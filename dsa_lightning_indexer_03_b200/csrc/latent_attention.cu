@@ -120,9 +120,11 @@ int64_t max_groups(int64_t T, int64_t B, int64_t H) {
 Ws carve(void* base, int64_t T, int64_t B, int64_t H, int blocks) {
   Ws w;
   w.max_groups = max_groups(T, B, H);
+  // parts 256 bytes apart from a 256-byte boundary, wherever the workspace itself starts
+  uint8_t* const start = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(base) + 255) & ~uintptr_t(255));
   int64_t off = 0;
   auto take = [&](int64_t bytes) {
-    uint8_t* p = static_cast<uint8_t*>(base) + off;
+    uint8_t* p = start + off;
     off = (off + bytes + 255) & ~int64_t(255);
     return p;
   };
@@ -134,7 +136,7 @@ Ws carve(void* base, int64_t T, int64_t B, int64_t H, int blocks) {
   w.merge = reinterpret_cast<Merge*>(take(sizeof(Merge) * blocks));
   w.ml = reinterpret_cast<float2*>(take(sizeof(float2) * kRows * 2 * blocks));
   w.o = reinterpret_cast<float*>(take(4 * kSlotFloats * 2 * blocks));
-  w.bytes = off;
+  w.bytes = off + 256;
   return w;
 }
 

@@ -29,7 +29,10 @@
 //   joins the pieces of an item.
 //
 // Bound: the tensor core, 128 x 128 x (192 + 128) products in 1,280 cycles, and close behind
-// it the 16,384 exponentials of those weights (1,024 cycles).
+// it the 16,384 exponentials of those weights (1,024 cycles).  Measured: a step of both tiles takes
+// 3,950 cycles, the chain of one of them (scores 1,400, maximum 550, weights 1,500, rest of the
+// sums 500), and changing items 15,000; 8,192 tokens x 96 heads 2.18 ms in a row of calls, of
+// which the up-projection is 0.21 (1.37 and 0.13 at the measured tensor rate).
 
 #include <cuda_fp16.h>
 
@@ -92,9 +95,11 @@ Ws carve(void* base, int64_t T, int64_t B, int64_t H, int64_t cache_rows, int bl
   Ws w;
   w.max_pairs = T / kPair + (B < T ? B : T) + 1;
   w.max_tiles = cache_rows / kTok + (B < T ? B : T) + 1;
+  // parts 256 bytes apart from a 256-byte boundary, wherever the workspace itself starts
+  uint8_t* const start = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(base) + 255) & ~uintptr_t(255));
   int64_t off = 0;
   auto take = [&](int64_t bytes) {
-    uint8_t* p = static_cast<uint8_t*>(base) + off;
+    uint8_t* p = start + off;
     off = (off + bytes + 255) & ~int64_t(255);
     return p;
   };
@@ -110,7 +115,7 @@ Ws carve(void* base, int64_t T, int64_t B, int64_t H, int64_t cache_rows, int bl
   w.ml = reinterpret_cast<float2*>(take(sizeof(float2) * kPair * 2 * blocks));
   w.o = reinterpret_cast<float*>(take(int64_t(4) * kPair * 128 * 2 * blocks));
   w.kv = take(w.max_tiles * H * kKvBytes);
-  w.bytes = off;
+  w.bytes = off + 256;
   return w;
 }
 

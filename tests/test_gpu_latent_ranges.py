@@ -241,3 +241,34 @@ def test_prompt_then_decode_through_one_cache(dsa, ix):
     ref, lref, mag = oracle.latent_attention(f64(d.q), f64(back), d.pos.numpy(), [0, 4], [0, n], SCALE)
     assert np.all(np.abs(o4 - o) <= 2.02 * U * np.abs(ref) + (1.01 * U + 1.1 * F + 1e-4) * (mag + np.abs(ref)) + 1e-5)
     assert np.all(np.abs(l4 - lse) <= 1e-4) and np.all(np.abs(lse - lref) <= 1e-4)
+
+
+def test_a_workspace_at_any_16_bytes(dsa, ix):
+    import ctypes
+    from dsa_lightning_indexer_03_b200 import _lib
+    lib = _lib.load()
+    p = lambda t: ctypes.c_void_p(t.data_ptr())  # noqa: E731
+    for n, nq, H in ((300, 140, 4), (2500, 300, 3)):
+        b, w = Batch(90, [n], [nq], H, dim=192), _weights(33, H).to(DEV)
+        q, kv, pos, qo, co = b.dev("q", "kv", "pos", "qo", "co")
+        want = ix.latent_attention_expanded(q, kv, w, pos, qo, co, SCALE)
+        need = lib.dsa_indexer_latent_expanded_workspace(ix._h, nq, 1, H, n)
+        ws = torch.empty(need + 256, dtype=torch.uint8, device=DEV)
+        for off in (16, 48, 240):
+            out = torch.zeros_like(want)
+            torch.cuda.synchronize()
+            st = lib.dsa_indexer_latent_attention_expanded(ix._h, nq, p(q), H, p(kv), n, p(w), p(pos), p(qo), 1, p(co), SCALE,
+                                                           p(out), ctypes.c_void_p(ws.data_ptr() + off), need, None)
+            torch.cuda.synchronize()
+            assert st == dsa.DSA_OK and ix.device_error() == dsa.DSA_OK and torch.equal(out, want)
+        d = Batch(91, [n], [2], H)
+        q, kv, pos, qo, co = d.dev("q", "kv", "pos", "qo", "co")
+        want, lse = ix.latent_attention(q, kv, pos, qo, co, SCALE)
+        need = lib.dsa_indexer_latent_attention_workspace(ix._h, 2, 1, H)
+        out, l2 = torch.zeros_like(want), torch.zeros_like(lse)
+        ws = torch.empty(need + 256, dtype=torch.uint8, device=DEV)
+        torch.cuda.synchronize()
+        st = lib.dsa_indexer_latent_attention(ix._h, 2, p(q), H, p(kv), n, p(pos), p(qo), 1, p(co), SCALE, p(out), p(l2),
+                                              ctypes.c_void_p(ws.data_ptr() + 48), need, None)
+        torch.cuda.synchronize()
+        assert st == dsa.DSA_OK and torch.equal(out, want) and torch.equal(l2, lse)
