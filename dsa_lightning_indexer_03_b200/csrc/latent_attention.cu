@@ -1042,9 +1042,8 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
 }
 
 // ---------------------------------------------------------------- merge
-// Rows of the groups that several blocks share, from the pieces in the order of their tiles, four
-// rows a block at a time, so that their loads are in flight together; with malformed offsets, rows of the call as attending to nothing.
-constexpr int kMergeThreads = 128, kMergeRows = 4;
+// Rows of the groups that several blocks share, from the pieces in a fixed order; with malformed offsets, rows of the call as attending to nothing.
+constexpr int kMergeThreads = 128, kMergeRows = 2;
 
 // Row `row` of out from its own prefix alone, by the block: scores of 128 tokens at a time, a
 // thread each, then four of the 512 dims a thread.  For rows that a NaN or an infinity beside
@@ -1108,29 +1107,43 @@ __global__ void __launch_bounds__(kMergeThreads) latent_merge_kernel(Params p, i
     return;
   }
   for (int k = blockIdx.x; k < plan.spoiled; k += gridDim.x) redo_row(p, w.spoiled[k]);
+  // two rows a block, a warp for every fourth piece (a long sequence alone has one from every block),
+  // then the warps' sums
+  __shared__ float4 so[kMergeThreads / 32][kMergeRows][kLatV / 4];
+  __shared__ float2 sml[kMergeThreads / 32][kMergeRows];
+  const int warp = tid >> 5, lane = tid & 31;
   for (int item = blockIdx.x; item < plan.merges * (kRows / kMergeRows); item += gridDim.x) {
     const Merge mg = w.merge[item / (kRows / kMergeRows)];
     const int r0 = item % (kRows / kMergeRows) * kMergeRows;
     if (r0 >= mg.nrows) continue;
-    // pieces: the tail slot of the first block, then the head slots of the others
+    // pieces: the tail slot of the first block, then the head slots of the others; with fewer tiles
+    // than blocks a share is one tile or empty, and the blocks are found from the tiles
+    const bool few = plan.tiles < blocks;
+    int64_t x0 = 0, x1 = 0, y;
+    if (few) {
+      share(plan.tiles, mg.first, blocks, &x0, &y);
+      share(plan.tiles, mg.last, blocks, &x1, &y);
+    }
+    const int pieces = few ? static_cast<int>(x1 - x0) + 1 : mg.last - mg.first + 1;
     float m[kMergeRows], l[kMergeRows];
-    float4 o[kMergeRows];
+    float4 o[kMergeRows][4];
 #pragma unroll
-    for (int r = 0; r < kMergeRows; ++r) m[r] = kUnset, l[r] = 0.f, o[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int r = 0; r < kMergeRows; ++r) {
+      m[r] = kUnset, l[r] = 0.f;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) o[r][d] = make_float4(0.f, 0.f, 0.f, 0.f);
+    }
 #pragma unroll 2
-    for (int k = mg.first; k <= mg.last; ++k) {
-      if (plan.tiles < blocks) {      // with fewer tiles than blocks some shares are empty
-        int64_t x, y;
-        share(plan.tiles, k, blocks, &x, &y);
-        if (x >= y) continue;
-      }
+    for (int n = warp; n < pieces; n += kMergeThreads / 32) {
+      const int k = few ? share_of(plan.tiles, x0 + n, blocks) : mg.first + n;
       const int64_t at = static_cast<int64_t>(2 * k + (k == mg.first)) * kRows + r0;
       float2 v[kMergeRows];
-      float4 c[kMergeRows];
+      float4 c[kMergeRows][4];
 #pragma unroll
       for (int r = 0; r < kMergeRows; ++r) {
         v[r] = w.ml[at + r];
-        c[r] = reinterpret_cast<const float4*>(w.o + (at + r) * kLatV)[tid];
+#pragma unroll
+        for (int d = 0; d < 4; ++d) c[r][d] = reinterpret_cast<const float4*>(w.o + (at + r) * kLatV)[lane + 32 * d];
       }
 #pragma unroll
       for (int r = 0; r < kMergeRows; ++r) {
@@ -1138,21 +1151,45 @@ __global__ void __launch_bounds__(kMergeThreads) latent_merge_kernel(Params p, i
         const float now = fmaxf(m[r], v[r].x), f0 = ex2_approx(m[r] - now), f1 = ex2_approx(v[r].x - now);
         m[r] = now;
         l[r] = fmaf(l[r], f0, v[r].y * f1);
-        o[r].x = fmaf(o[r].x, f0, c[r].x * f1);
-        o[r].y = fmaf(o[r].y, f0, c[r].y * f1);
-        o[r].z = fmaf(o[r].z, f0, c[r].z * f1);
-        o[r].w = fmaf(o[r].w, f0, c[r].w * f1);
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+          o[r][d].x = fmaf(o[r][d].x, f0, c[r][d].x * f1);
+          o[r][d].y = fmaf(o[r][d].y, f0, c[r][d].y * f1);
+          o[r][d].z = fmaf(o[r][d].z, f0, c[r][d].z * f1);
+          o[r][d].w = fmaf(o[r][d].w, f0, c[r][d].w * f1);
+        }
       }
     }
+    __syncthreads();                          // so is free again
 #pragma unroll
     for (int r = 0; r < kMergeRows; ++r) {
-      if (r0 + r >= mg.nrows) break;
-      const float inv = l[r] != 0.f ? 1.f / l[r] : 0.f;
+#pragma unroll
+      for (int d = 0; d < 4; ++d) so[warp][r][lane + 32 * d] = o[r][d];
+      if (lane == 0) sml[warp][r] = make_float2(m[r], l[r]);
+    }
+    __syncthreads();
+    for (int r = 0; r < kMergeRows && r0 + r < mg.nrows; ++r) {
+      float mm = kUnset, ll = 0.f;
+      for (int k = 0; k < kMergeThreads / 32; ++k)
+        if (sml[k][r].y != 0.f) mm = fmaxf(mm, sml[k][r].x);
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+      for (int k = 0; k < kMergeThreads / 32; ++k) {
+        const float2 v = sml[k][r];
+        if (v.y == 0.f) continue;
+        const float f = ex2_approx(v.x - mm);
+        const float4 c = so[k][r][tid];
+        ll = fmaf(v.y, f, ll);
+        a.x = fmaf(c.x, f, a.x);
+        a.y = fmaf(c.y, f, a.y);
+        a.z = fmaf(c.z, f, a.z);
+        a.w = fmaf(c.w, f, a.w);
+      }
+      const float inv = ll != 0.f ? 1.f / ll : 0.f;
       const int64_t row = mg.row0 + r0 + r;
       reinterpret_cast<uint2*>(p.out + row * kLatV)[tid] =
-          l[r] != 0.f ? make_uint2(pack2(o[r].x * inv, o[r].y * inv), pack2(o[r].z * inv, o[r].w * inv)) : make_uint2(0u, 0u);
-      if (tid == 0) p.lse[row] = l[r] != 0.f ? fmaf(m[r], 0.69314718055994531f, logf(l[r])) : -INFINITY;
-      const bool nan = l[r] == l[r] && l[r] != 0.f && !(o[r].x == o[r].x && o[r].y == o[r].y && o[r].z == o[r].z && o[r].w == o[r].w);
+          ll != 0.f ? make_uint2(pack2(a.x * inv, a.y * inv), pack2(a.z * inv, a.w * inv)) : make_uint2(0u, 0u);
+      if (tid == 0) p.lse[row] = ll != 0.f ? fmaf(mm, 0.69314718055994531f, logf(ll)) : -INFINITY;
+      const bool nan = ll == ll && ll != 0.f && !(a.x == a.x && a.y == a.y && a.z == a.z && a.w == a.w);
       if (p.kv && __syncthreads_or(nan)) redo_row(p, row);
     }
   }
