@@ -8,7 +8,8 @@ Readings ('Latent attention (MLA)' row: 512-dim latent plus a 64-dim shared key 
   * dense: query t at position p attends to rows 0..p of its own sequence; p = -1 to nothing
     (o = 0, lse = -inf); score = scale * (q . row) over the 576 cached values, value = latent;
   * expanded: a head's key is the bf16 up-projection of the latent (128 values) followed by the
-    row's 64 rope values, its value the bf16 up-projection (128 values);
+    row's 64 rope values, its value the bf16 up-projection (128 values); the library keeps both
+    in fp16 instead, and bounds that use this form allow a step of bf16 a value;
   * 4-bit rows: blocks of 16 latent values share the scale e4m3(min(amax / 6, 448)); codes are
     e2m1, nearest, ties to even, saturating; the rope key stays bf16.
 """
