@@ -151,6 +151,7 @@ struct Params {
   const int64_t* cache_offsets;
   const int32_t* idx;
   float scale_log2;
+  ScoreScale scale;            // the same, for scaled queries
   __nv_bfloat16* out;
   float* lse;
   Ws ws;
@@ -566,7 +567,7 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
               *reinterpret_cast<uint32_t*>(sQ + c * kQChunk + rr * 128 + (((lane >> 2) ^ (rr & 7)) * 16) + (lane & 3) * 4) =
                   c < 8 ? pack_f16(lo, hi) : pack2(lo, hi);
             }
-            if (lane == 0) mi.qs[segs & 1][rr] = p.scale_log2 * pow2(f);
+            if (lane == 0) mi.qs[segs & 1][rr] = score_factor(p.scale, f);
           }
           fence_proxy_async_smem();
           mbar_arrive(&mi.q_full);
@@ -1217,7 +1218,8 @@ cudaError_t launch_latent_attention(const LatentArgs& a, const CUtensorMap& tmQ,
   p.q_seq_offsets = a.q_seq_offsets;
   p.cache_offsets = a.cache_offsets;
   p.idx = a.idx;
-  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.scale_log2 = scale_to_log2(a.scale);
+  p.scale = score_scale(p.scale_log2);
   p.out = static_cast<__nv_bfloat16*>(a.out);
   p.lse = a.lse;
   p.ws = carve(a.workspace, a.T, a.B, a.H, blocks);

@@ -128,7 +128,7 @@ struct Params {
   const int32_t* positions;
   const int32_t* q_seq_offsets;
   const int64_t* cache_offsets;
-  float scale_log2;
+  ScoreScale scale;             // times log2(e)
   __nv_bfloat16* out;
   Ws ws;
   int* err;
@@ -561,7 +561,7 @@ __device__ __noinline__ void redo_half_row(const Params& p, int tile0, int64_t r
     for (int d = 0; d < 192; ++d)
       x = fmaf(__bfloat162float(q[d]),
                __half2float(*reinterpret_cast<const __half*>(kv + (d >> 6) * kChunk + r * 128 + ((((d & 63) >> 3) ^ (r & 7)) * 16) + (d & 7) * 2)), x);
-    x *= p.scale_log2 * pow2(static_cast<int>(sc.x));
+    x *= score_factor(p.scale, static_cast<int>(sc.x));
     const float top = fmaxf(m, x), f = m == -INFINITY ? 0.f : ex2_approx(m - top);
     const float wt = top == -INFINITY ? 0.f : ex2_approx(x - top);
     l = fmaf(l, f, wt);
@@ -812,7 +812,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
         lim = p.positions[pc.pr.tok0 + tok];
         if (lim < -1 || lim >= pc.pr.seq_len) lim = -1;
       }
-      float a = 0.f;
+      int fq = 0;                                         // exponent of the row's scale
       if (n > 0) {
         // the warp's 32 rows of Q in fp16: lane l holds values 2l, 2l + 1 of each 64 of a row; all
         // of them are in flight at once
@@ -836,7 +836,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
           for (int c = 0; c < 3; ++c)
             *reinterpret_cast<uint32_t*>(sQ + i * kQTile + c * kChunk + rr * 128 + (((lane >> 2) ^ (rr & 7)) * 16) + (lane & 3) * 4) =
                 pack_f16(__uint_as_float(v[k][c] << 16) * inv, __uint_as_float(v[k][c] & 0xFFFF0000u) * inv);
-          if (lane == k) a = p.scale_log2 * pow2(f);
+          if (lane == k) fq = f;
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -849,7 +849,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
       if (n > 0) sc = scales[0];
 #pragma unroll 1
       for (int t = 0; t < n; ++t, ++done) {
-        const float ak = a * pow2(static_cast<int>(sc.x)), fv = sc.y;
+        const float ak = score_factor(p.scale, fq + static_cast<int>(sc.x)), fv = sc.y;
         if (t + 1 < n) sc = scales[static_cast<int64_t>(t + 1) * p.H];
         const int pos0 = (pc.t0 + t) * kTok;
         ok = ok && __all_sync(0xffffffffu, mbar_wait(&mi.s_full[i], done & 1, wc));
@@ -1081,7 +1081,7 @@ cudaError_t launch_latent_expanded(const ExpandedArgs& a, const CUtensorMap& tmC
   p.positions = a.positions;
   p.q_seq_offsets = a.q_seq_offsets;
   p.cache_offsets = a.cache_offsets;
-  p.scale_log2 = a.scale * 1.4426950408889634f;
+  p.scale = score_scale(scale_to_log2(a.scale));
   p.out = static_cast<__nv_bfloat16*>(a.out);
   p.ws = carve(a.workspace, a.T, a.B, a.H, a.cache_rows, blocks);
   p.err = a.err;

@@ -2,6 +2,9 @@
 // blocks' shares, and tensor-core helpers whose operands stay in uniform registers.
 #pragma once
 
+#include <cfloat>
+#include <cmath>
+
 #include "common.cuh"
 
 namespace dsa {
@@ -145,8 +148,29 @@ __device__ __forceinline__ int scale_exponent(float top, int lowest) {
   const int e = static_cast<int>((__float_as_uint(top) >> 23) & 0xFF) - 127;
   return (e < lowest ? lowest : e) - 14;
 }
-// Of queries and keys: a factor of a score, down to where its product stays normal.  Of values: the
-// weights take the scale over, so those of one row's tiles must stay within fp32 of each other.
+// Of queries and keys: lifted as far as pow2(-f) reaches.  Of values: the weights take the scale over,
+// so those of one row's tiles must stay within fp32 of each other.
 constexpr int kLowestFactor = -106, kLowestValue = -60;
+
+// scale * log2(e) as m * 2^e, m in [1, 2): the factor of a score whose query and key were scaled by
+// 2^f in all is m * 2^(e + f).  The exponents are summed first, since 2^-120 of a zero query times
+// 2^-120 of a zero key is 0 in fp32, and a masked score of -inf times 0 is NaN.  Held at -126 below:
+// scaled products stay under 2^38, so such scores are 0 to fp32 either way.
+struct ScoreScale {
+  float m;
+  int e;
+};
+inline ScoreScale score_scale(float scale_log2) {
+  ScoreScale s;
+  s.m = 2.f * frexpf(scale_log2, &s.e);
+  --s.e;
+  return s;
+}
+// finite, so that a score of 0 stays 0
+inline float scale_to_log2(float scale) { return fminf(scale * 1.4426950408889634f, FLT_MAX); }
+__device__ __forceinline__ float score_factor(ScoreScale s, int f) {
+  const int e = s.e + f;
+  return s.m * pow2(e < -126 ? -126 : e > 127 ? 127 : e);
+}
 
 }  // namespace dsa

@@ -1,0 +1,158 @@
+"""Latent-cache operators on inputs at the ends of their number formats: zero queries and keys,
+factors of a score far below one, and values of very different magnitude beside each other.
+
+Tolerances (U = 2^-8 and F = 2^-11, the unit roundoffs of bf16 and fp16).  Everything a bound uses is
+taken over the rows that the query attends to, none over rows it does not.
+  * expanded: a key or value is rounded to fp16 under a scale that brings its row's largest
+    magnitude to at least 2^6 (a tile's scale serves rows within 2^8 of its largest; others carry
+    their own), so it is off by F of itself or, below fp16's normal range, by 2^-25 / 2^6 = 2^-31 of
+    the row's largest.  A score moves by e_k = scale sum_d |q_d| (F |k_d| + 2^-31 max|k|) at most, and by
+    the fp32 sums' e_s = 6 sqrt(192) 2^-24 scale |q| max|k| + 4 * 2^-24 max|x| + 2^-20.
+    A weight is off by F of itself or by 2^-25 where the largest product of a weight and its
+    value's scale is at least 2^7; scales are within 2^8 of what their row needs, so n such weights
+    add at most n 2^-32 2^9 2 = n 2^-22 of the largest w_s max|v_s|.  With e = e_k + e_s:
+    |o - o_ref| <= 1.01 U |o_ref| + (2.1 F + 2 expm1(e)) (mag + |o_ref|) + n 2^-22 max_s(w_s max|v_s|)
+                   + 2^-30 sum_s w_s max|v_s|,   mag = sum_s w_s |v_s|.
+  * 4-bit: values are exact, weights as above with the scales left out: n 2^-32 max|v|."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+import workloads as W
+from _parity import f64
+from test_gpu_latent import DEV, SCALE, U, Batch, _check, _quantized, _weights
+
+pytestmark = pytest.mark.gpu
+
+F = 2.0 ** -11
+
+
+@pytest.fixture(scope="module")
+def dsa():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from dsa_lightning_indexer_03_b200 import build
+    build.build()
+    import dsa_lightning_indexer_03_b200 as d
+    return d
+
+
+@pytest.fixture(scope="module")
+def ix(dsa):
+    wts = W.make_weights(41, hidden_dim=128, q_latent_dim=64)
+    return dsa.Indexer(*(t.to(DEV).contiguous() for t in (wts.W_q, wts.W_k, wts.W_w, wts.gamma, wts.beta)),
+                       max_tokens=4096)
+
+
+def _expanded(ix, b, w, scale=SCALE, **kw):
+    return f64(ix.latent_attention_expanded(*b.dev("q", "kv"), w.to(DEV), *b.dev("pos", "qo", "co"), scale, **kw))
+
+
+def _check_seen(o, b, w, scale=SCALE, tokens=None):
+    """o against the definition in 64 bits, each query from the rows it attends to alone."""
+    q, kv, wd = f64(b.q), f64(b.kv), f64(w)
+    pos, qo, co = b.pos.numpy(), b.qo.numpy(), b.co.numpy()
+    for s in range(len(qo) - 1):
+        r0 = int(co[s])
+        ts = [t for t in range(int(qo[s]), int(qo[s + 1])) if tokens is None or t in tokens]
+        n = max([int(pos[t]) + 1 for t in ts], default=0)
+        c = kv[r0:r0 + n]
+        for h in range(q.shape[1]):
+            with np.errstate(all="ignore"):                  # rows that none of these queries sees whole
+                k_all = np.concatenate((c[:, :512] @ wd[h, :128].T, c[:, 512:]), axis=1)
+                v_all = c[:, :512] @ wd[h, 128:].T
+            for t in ts:
+                m = int(pos[t]) + 1
+                if m == 0:
+                    assert np.all(o[t, h] == 0)
+                    continue
+                k, v = k_all[:m], v_all[:m]
+                x = scale * (k @ q[t, h])
+                wt = np.exp(x - x.max())
+                wt /= wt.sum()
+                ref, mag, vmax, kmax = wt @ v, wt @ np.abs(v), np.abs(v).max(1), np.abs(k).max(1)
+                e = scale * (np.abs(k) @ np.abs(q[t, h]) * F + 2.0 ** -31 * kmax * np.abs(q[t, h]).sum())
+                e = e[wt > 1e-12].max()                      # a lighter row's move does not show
+                e += 6 * np.sqrt(192) * 2.0 ** -24 * scale * np.linalg.norm(q[t, h]) * np.linalg.norm(k[wt > 1e-12], axis=1).max()
+                e += 4 * 2.0 ** -24 * np.abs(x[wt > 1e-12]).max() + 2.0 ** -20
+                tol = 1.01 * U * np.abs(ref) + (2.1 * F + 2 * np.expm1(e)) * (mag + np.abs(ref))
+                tol += m * 2.0 ** -22 * (wt * vmax).max() + 2.0 ** -30 * (wt * vmax).sum() + 1e-38
+                err = np.abs(o[t, h] - ref)
+                assert np.all(err <= tol), (t, h, err.max(), (err / tol).max())
+
+
+def _shared(seed, n, nq, H):
+    """A batch of one sequence beside two more, with few heads (shares of steps) or many (whole items)."""
+    return Batch(seed, [n, 140], [nq, 20], H, dim=192), _weights(seed, H)
+
+
+# ------------------------------------------------------------------------------ factors of a score
+
+@pytest.mark.parametrize("what", ["q", "kv", "both", "a query", "a row", "a tile"])
+@pytest.mark.parametrize("H", [2, 300])
+def test_expanded_zeros(dsa, ix, what, H):
+    b, w = _shared(101, 300, 150 if H == 2 else 40, H)
+    if what in ("q", "both"):
+        b.q.zero_()
+    if what in ("kv", "both"):
+        b.kv.zero_()
+    if what == "a query":
+        b.q[7] = 0
+        b.q[3, 1] = 0
+    if what == "a row":
+        b.kv[5] = 0
+        b.kv[131, 512:] = 0
+    if what == "a tile":
+        b.kv[128:256] = 0
+        b.q[9] = 0
+    o = _expanded(ix, b, w)
+    assert ix.device_error() == dsa.DSA_OK
+    _check_seen(o, b, w, tokens=None if H == 2 else {3, 7, 9, 39, 50})
+    one = Batch(1, [1], [1], 1, dim=192)                     # a first token over a cache of zeros
+    one.q.zero_(), one.kv.zero_()
+    assert np.all(_expanded(ix, one, _weights(1, 1)) == 0)
+
+
+@pytest.mark.parametrize("q_exp,kv_exp,s_exp", [(-60, -60, 0), (-100, -14, 0), (0, 0, -100), (0, 0, -120), (-100, 0, -20),
+                                                (20, 20, -40), (-60, -60, 120)])
+def test_expanded_factors_far_from_one(dsa, ix, q_exp, kv_exp, s_exp):
+    b, w = _shared(102, 290, 100, 2)
+    b.q = (b.q.float() * 2.0 ** q_exp).to(torch.bfloat16)
+    b.kv = (b.kv.float() * 2.0 ** kv_exp).to(torch.bfloat16)
+    b.q[4] = 0
+    scale = SCALE * 2.0 ** s_exp
+    o = _expanded(ix, b, w, scale)
+    assert ix.device_error() == dsa.DSA_OK
+    _check_seen(o, b, w, scale)
+
+
+@pytest.mark.parametrize("s_exp", [0, -100, -125])
+def test_4bit_zero_queries_and_small_scales(dsa, ix, s_exp):
+    b = Batch(103, [300, 90], [3, 2], 24)
+    b.q[1] = 0
+    b.q[3, 5] = 0
+    kv4, val = _quantized(b.kv)
+    val[7], kv4[7] = 0, 0
+    q, pos, qo, co = b.dev("q", "pos", "qo", "co")
+    scale = 0.0625 * 2.0 ** s_exp
+    o, lse = ix.latent_attention_fp4(q, kv4.to(DEV), pos, qo, co, scale)
+    assert ix.device_error() == dsa.DSA_OK
+    _check(f64(o), f64(lse), f64(b.q), val, b.pos.numpy(), b.qo.numpy(), b.co.numpy(), scale=scale)
+
+
+def test_scales_at_the_end_of_the_range(dsa, ix):
+    # a product of the largest scale with ln 2's inverse overflows: zero scores must stay zero
+    b = Batch(104, [200], [2], 8)
+    b.q.zero_()
+    kv4, val = _quantized(b.kv)
+    q, kv, pos, qo, co = b.dev("q", "kv", "pos", "qo", "co")
+    for scale in (3.0e38, 2.0 ** -126, 1e-41):
+        for o, lse, rows in ((*ix.latent_attention(q, kv, pos, qo, co, scale), f64(b.kv)),
+                             (*ix.latent_attention_fp4(q, kv4.to(DEV), pos, qo, co, scale), val)):
+            _check(f64(o), f64(lse), f64(b.q), rows, b.pos.numpy(), b.qo.numpy(), b.co.numpy(), scale=scale)
+        e, w = Batch(105, [200], [2], 3, dim=192), _weights(3, 3)
+        e.q.zero_()
+        _check_seen(_expanded(ix, e, w, scale), e, w, scale)
+    assert ix.device_error() == dsa.DSA_OK
