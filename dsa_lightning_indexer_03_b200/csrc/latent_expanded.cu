@@ -714,10 +714,10 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
             ++iv;
           }
         }
-        if (!ok) {   // the loads in flight land before the block ends
-          for (uint32_t k = ik > kKStages ? ik - kKStages : 0; k < ik; ++k) drain(&mi.full_k[k % kKStages], (k / kKStages) & 1);
-          for (uint32_t k = iv > kVStages ? iv - kVStages : 0; k < iv; ++k) drain(&mi.full_v[k % kVStages], (k / kVStages) & 1);
-        }
+        // the loads in flight land before the block ends, also when next() gave up waiting; after the
+        // last item they have landed and this takes no time
+        for (uint32_t k = ik > kKStages ? ik - kKStages : 0; k < ik; ++k) drain(&mi.full_k[k % kKStages], (k / kKStages) & 1);
+        for (uint32_t k = iv > kVStages ? iv - kVStages : 0; k < iv; ++k) drain(&mi.full_v[k % kVStages], (k / kVStages) & 1);
       }
       __syncwarp();
     } else if (warp < 3) {
