@@ -68,7 +68,7 @@ struct Plan {
   int32_t pairs, tiles;     // entries of Ws::pair and Ws::step
   int64_t steps;            // over all pairs, of one head
   int32_t bad, merges;
-  int32_t next, pad;
+  int32_t next, spoiled;    // items handed out; entries of Ws::spoiled
 };
 
 struct Merge {
@@ -84,6 +84,7 @@ struct Ws {
   int64_t* step0;       // [max pairs + 1] steps before each pair
   Steps* step;          // [max tiles]
   Merge* merge;         // [blocks]
+  int2* spoiled;        // [T * H] a row of out to compute again, and the entry before it of the same warp
   float2* scale;        // [max tiles][H] exponents of the key and value scales
   float2* ml;           // [2 * blocks][256] reference and sum of a piece's rows
   float* o;             // [2 * blocks][256][128]
@@ -111,6 +112,7 @@ Ws carve(void* base, int64_t T, int64_t B, int64_t H, int64_t cache_rows, int bl
   w.step0 = reinterpret_cast<int64_t*>(take(8 * (w.max_pairs + 1)));
   w.step = reinterpret_cast<Steps*>(take(sizeof(Steps) * w.max_tiles));
   w.merge = reinterpret_cast<Merge*>(take(sizeof(Merge) * blocks));
+  w.spoiled = reinterpret_cast<int2*>(take(sizeof(int2) * T * H));
   w.scale = reinterpret_cast<float2*>(take(sizeof(float2) * w.max_tiles * H));
   w.ml = reinterpret_cast<float2*>(take(sizeof(float2) * kPair * 2 * blocks));
   w.o = reinterpret_cast<float*>(take(int64_t(4) * kPair * 128 * 2 * blocks));
@@ -545,38 +547,61 @@ __device__ __forceinline__ void item_of(const Params& p, uint32_t pairs, uint32_
   *head = g * group + rest % in;
 }
 
-// Row (t, h) of out over its own prefix, half of the dims, by one thread: for rows that a NaN or
-// an infinity beside their prefix spoiled (0 * NaN).
-__device__ __noinline__ void redo_half_row(const Params& p, int tile0, int64_t row, int head, int lim, int half) {
-  const __nv_bfloat16* const q = p.q + row * 192;
-  float m = -INFINITY, l = 0.f, o[64];
-#pragma unroll
-  for (int d = 0; d < 64; ++d) o[d] = 0.f;
-  for (int s = 0; s <= lim; ++s) {
-    const int64_t blk = static_cast<int64_t>(tile0 + s / kTok) * p.H + head;
+// Row (token, head) of out over its own prefix, by a warp: scores of 32 tokens at a time, a lane
+// each, then four of the 128 dims a lane.  For rows that a NaN or an infinity beside their prefix
+// spoiled (0 * NaN).  It may take long, so it runs where nobody waits for the warp.
+__device__ __noinline__ void redo_row(const Params& p, int row) {
+  const int lane = threadIdx.x & 31, t = row / p.H, head = row - t * p.H;
+  const int tile0 = p.ws.seq_tile[last_at(p.q_seq_offsets, p.B, t)], lim = p.positions[t];
+  const uint4* const q = reinterpret_cast<const uint4*>(p.q + static_cast<int64_t>(row) * 192);
+  float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
+  for (int s0 = 0; s0 <= lim; s0 += 32) {
+    const int64_t blk = static_cast<int64_t>(tile0 + s0 / kTok) * p.H + head;
     const uint8_t* const kv = p.ws.kv + blk * kKvBytes;
     const float2 sc = p.ws.scale[blk];
-    const int r = s % kTok;
-    float x = 0.f;
-    for (int d = 0; d < 192; ++d)
-      x = fmaf(__bfloat162float(q[d]),
-               __half2float(*reinterpret_cast<const __half*>(kv + (d >> 6) * kChunk + r * 128 + ((((d & 63) >> 3) ^ (r & 7)) * 16) + (d & 7) * 2)), x);
-    x *= score_factor(p.scale, static_cast<int>(sc.x));
-    const float top = fmaxf(m, x), f = m == -INFINITY ? 0.f : ex2_approx(m - top);
-    const float wt = top == -INFINITY ? 0.f : ex2_approx(x - top);
-    l = fmaf(l, f, wt);
-    m = top;
-    const float vs = pow2(static_cast<int>(sc.y));
+    const int r0 = s0 % kTok, r = r0 + lane, n = lim - s0 < 31 ? lim - s0 + 1 : 32;
+    float x = -INFINITY;
+    if (lane < n) {
+      x = 0.f;
+#pragma unroll 4
+      for (int u = 0; u < 24; ++u) {
+        const uint4 a = q[u], k = *reinterpret_cast<const uint4*>(kv + (u >> 3) * kChunk + r * 128 + (((u & 7) ^ (r & 7)) * 16));
+        const uint32_t av[4] = {a.x, a.y, a.z, a.w}, kvw[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
-    for (int d = 0; d < 64; ++d) {
-      const float v = __half2float(*reinterpret_cast<const __half*>(kv + (3 + half) * kChunk + r * 128 + (((d >> 3) ^ (r & 7)) * 16) + (d & 7) * 2)) * vs;
-      o[d] = fmaf(o[d], f, wt * v);
+        for (int j = 0; j < 4; ++j) {
+          const float2 kf = __half22float2(*reinterpret_cast<const __half2*>(&kvw[j]));
+          x = fmaf(__uint_as_float(av[j] << 16), kf.x, fmaf(__uint_as_float(av[j] & 0xFFFF0000u), kf.y, x));
+        }
+      }
+      x *= score_factor(p.scale, static_cast<int>(sc.x));
+    }
+    float top = x;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    top = fmaxf(m, top);
+    const float f = m == -INFINITY ? 0.f : ex2_approx(m - top), wt = top == -INFINITY ? 0.f : ex2_approx(x - top);
+    m = top;
+    float sum = wt;
+#pragma unroll
+    for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+    l = fmaf(l, f, sum);
+#pragma unroll
+    for (int k = 0; k < 4; ++k) o[k] *= f;
+    const float wv = wt * pow2(static_cast<int>(sc.y));
+    for (int j = 0; j < n; ++j) {
+      const float w = __shfl_sync(0xffffffffu, wv, j);
+      const int rj = r0 + j;
+      const uint2 v = *reinterpret_cast<const uint2*>(kv + (3 + (lane >> 4)) * kChunk + rj * 128 +
+                                                      ((((lane & 15) >> 1) ^ (rj & 7)) * 16) + (lane & 1) * 8);
+      const float2 v0 = __half22float2(*reinterpret_cast<const __half2*>(&v.x)), v1 = __half22float2(*reinterpret_cast<const __half2*>(&v.y));
+      o[0] = fmaf(w, v0.x, o[0]);
+      o[1] = fmaf(w, v0.y, o[1]);
+      o[2] = fmaf(w, v1.x, o[2]);
+      o[3] = fmaf(w, v1.y, o[3]);
     }
   }
   const float inv = l != 0.f ? 1.f / l : 0.f;
-  uint32_t* const dst = reinterpret_cast<uint32_t*>(p.out + row * 128 + 64 * half);
-#pragma unroll
-  for (int d = 0; d < 32; ++d) dst[d] = pack2(o[2 * d] * inv, o[2 * d + 1] * inv);
+  reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(row) * 128)[lane] = make_uint2(pack2(o[0] * inv, o[1] * inv), pack2(o[2] * inv, o[3] * inv));
 }
 
 __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_constant__ Params p) {
@@ -801,6 +826,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
     const uint32_t tlane = tmem + (static_cast<uint32_t>(qd * 32) << 16);
     const uint32_t ts = tlane + 128 * i, to = tlane + kTmemSum + 128 * i;
     uint32_t done = 0, segs = 0, theirs = 0;              // steps of this tile, pieces, steps of the other
+    int spoiled = -1;                                     // lane 0: the warp's last entry of Ws::spoiled
     bool ok = true;
     while (ok && next(&pc, false)) {
       const int n = steps_of(pc, i), other = steps_of(pc, 1 - i);
@@ -957,14 +983,12 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
         if (real && whole) {
           uint4 v[4];
           uint32_t* const u = reinterpret_cast<uint32_t*>(v);
-          float zero = 0.f;        // NaN if a value is
 #pragma unroll
           for (int k = 0; k < 16; ++k) {
             const float v0 = __uint_as_float(o[2 * k]) * inv, v1 = __uint_as_float(o[2 * k + 1]) * inv;
-            zero = fmaf(v0, 0.f, fmaf(v1, 0.f, zero));
+            nan |= v0 != v0 || v1 != v1;
             u[k] = pack2(v0, v1);
           }
-          nan |= zero != 0.f;
           __nv_bfloat16* const dst = p.out + row * 128 + 32 * c;
           if ((reinterpret_cast<uintptr_t>(p.out) & 16) == 0) {
             store32(dst, v[0], v[1]);
@@ -987,11 +1011,20 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
         __syncwarp();
         if (lane == 0) mbar_arrive(&mi.o_free[i]);
       }
-      if (nan && inv == inv) {
-        redo_half_row(p, pc.pr.tile0, row, pc.head, lim, 0);
-        redo_half_row(p, pc.pr.tile0, row, pc.head, lim, 1);
+      for (unsigned bad = __ballot_sync(0xffffffffu, nan && inv == inv); bad; bad &= bad - 1) {
+        if (lane == 0) {
+          const int e = atomicAdd(&w.plan->spoiled, 1);
+          w.spoiled[e] = make_int2((pc.pr.tok0 + i * kRowsT + qd * 32 + __ffs(bad) - 1) * p.H + pc.head, spoiled);
+          spoiled = e;
+        }
       }
       __syncwarp();
+    }
+    // the warp's spoiled rows, when no other role waits for it any more
+    for (int e = __shfl_sync(0xffffffffu, spoiled, 0); e >= 0;) {
+      const int2 s = w.spoiled[e];
+      redo_row(p, s.x);
+      e = s.y;
     }
   }
   tc_fence_before();
@@ -1056,8 +1089,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_expanded_kernel(const __g
       reinterpret_cast<uint2*>(p.out + row * 128)[lane] =
           l[r] != 0.f ? make_uint2(pack2(o[r].x * inv, o[r].y * inv), pack2(o[r].z * inv, o[r].w * inv)) : make_uint2(0u, 0u);
       const bool nan = inv == inv && l[r] != 0.f && !(o[r].x == o[r].x && o[r].y == o[r].y && o[r].z == o[r].z && o[r].w == o[r].w);
-      if (__any_sync(0xffffffffu, nan) && lane < 2) redo_half_row(p, pr.tile0, row, mg.head, p.positions[pr.tok0 + tok + r], lane);
-      __syncwarp();
+      if (__any_sync(0xffffffffu, nan)) redo_row(p, static_cast<int>(row));   // each lane writes what it wrote above
     }
   }
 }

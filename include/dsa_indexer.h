@@ -353,7 +353,8 @@ dsa_status_t dsa_indexer_latent_attention_fp4(dsa_indexer_t h, int64_t T, const 
 
 /* Bytes of workspace of dsa_indexer_latent_attention_expanded (-1 for a bad argument): the keys
  * and values of all heads, 640 bytes a cache row and head with every sequence's rows filled up to
- * 128 ((cache_rows / 128 + min(B, T) + 1) * n_heads * 81,920 bytes), and some 40 MB more. */
+ * 128 ((cache_rows / 128 + min(B, T) + 1) * n_heads * 81,920 bytes), 8 bytes a query and head, and some
+ * 40 MB more. */
 int64_t dsa_indexer_latent_expanded_workspace(dsa_indexer_t h, int64_t T, int32_t B, int32_t n_heads,
                                               int64_t cache_rows);
 

@@ -156,3 +156,79 @@ def test_scales_at_the_end_of_the_range(dsa, ix):
         e.q.zero_()
         _check_seen(_expanded(ix, e, w, scale), e, w, scale)
     assert ix.device_error() == dsa.DSA_OK
+
+
+# ------------------------------------------------------------------------------ rows computed again
+
+_SLOW = """
+import os, sys
+os.environ["DSA_INDEXER_WAIT_TIMEOUT_MS"] = "20"
+sys.path.insert(0, %r)
+import torch, dsa_lightning_indexer_03_b200 as dsa
+g = torch.Generator(device="cuda").manual_seed(1)
+r = lambda *s: torch.randn(s, generator=g, device="cuda").to(torch.bfloat16)
+ix = dsa.Indexer(r(64, 4096), r(128, 128), r(128, 32), r(128), r(128), max_tokens=4096)
+i = lambda v, t=torch.int32: torch.tensor(v, dtype=t, device="cuda")
+for n, nq, H in ((30000, 200, 148), (30000, 200, 5)):
+    q, kv, w = r(nq, H, 192), r(n, 576), r(H, 256, 512) * 512 ** -0.5
+    pos, qo, co = torch.arange(n - nq, n, dtype=torch.int32, device="cuda"), i([0, nq]), i([0, n], torch.int64)
+    args = (w, pos, qo, co, 192 ** -0.5)
+    want = ix.latent_attention_expanded(q, kv, *args)
+    assert ix.device_error() == dsa.DSA_OK
+    kv[n - 40, 11] = float("nan")
+    got = ix.latent_attention_expanded(q, kv, *args)
+    assert ix.device_error() == dsa.DSA_OK, "timeout"
+    seen = pos >= n - 40
+    assert not bool(torch.isfinite(got[seen]).all(2).any())
+    # fp32 weights instead of fp16 ones: 2^-11 of a sum of magnitudes, and a rounding of out either way
+    d, m = (got - want)[~seen].float().abs(), want[~seen].float().abs()
+    assert bool((d <= 2 * 2.0 ** -8 * m + 2.0 ** -11 * 0.1).all()), float(d.max())
+print("fine")
+"""
+
+
+def test_expanded_rows_beside_a_nan_keep_nobody_waiting(dsa):
+    # a limit of 20 ms on every wait in the kernels: computing a row of 30,000 tokens again takes part
+    # in none (whole items and shares of steps)
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _SLOW % root], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "fine" in r.stdout, r.stdout + r.stderr
+
+
+def test_expanded_infinite_values_stay_and_nan_rows_are_right(dsa, ix):
+    # values of one head overflow to infinity while every score is finite: those outputs are
+    # infinite, the other dims as ordinary; repeated bit for bit
+    b, w = Batch(130, [600, 200], [300, 200], 3, dim=192), _weights(130, 3)
+    w[1, :128] = 0
+    w[1, 128 + 5] = 0
+    w[1, 128 + 5, 3] = 3.0e38
+    b.kv[:, 3] = 2.0
+    o = _expanded(ix, b, w)
+    assert ix.device_error() == dsa.DSA_OK
+    assert np.all(np.isposinf(o[:, 1, 5]))
+    assert np.all(np.isfinite(np.delete(o[:, 1], 5, axis=1))) and np.all(np.isfinite(o[:, [0, 2]]))
+    assert np.array_equal(o, _expanded(ix, b, w))
+    fin = w.clone()
+    fin[1, 128 + 5] = 0
+    # a query of a tile that also holds rows it does not see (0 * inf) is computed again with fp32
+    # weights instead of fp16 ones, so both results are held to the bound, not to each other's bits
+    o[:, 1, 5] = 0
+    _check_seen(o, b, fin)
+    _check_seen(_expanded(ix, b, fin), b, fin)
+
+
+@pytest.mark.parametrize("H", [3, 148])
+def test_expanded_many_rows_beside_a_nan(dsa, ix, H):
+    # whole tiles of queries in reverse order, most of which see neither of two broken rows
+    b, w = Batch(131, [1100, 300], [256, 140], H, dim=192), _weights(131, H)
+    b.pos = torch.cat((torch.arange(1099, 843, -1), torch.arange(299, 159, -1))).int()
+    b.kv[1090, 8] = float("inf")
+    b.kv[1100 + 250] = float("nan")
+    o = _expanded(ix, b, w)
+    assert ix.device_error() == dsa.DSA_OK
+    assert not np.any(np.isfinite(o[:10]).all(axis=2)) and not np.any(np.isfinite(o[256:306]).all(axis=2))
+    b.kv = torch.nan_to_num(b.kv, 0, 0, 0)
+    _check_seen(o, b, w, tokens={10, 11, 100, 127, 128, 255, 306, 307, 395})
