@@ -9,8 +9,10 @@
 // triple the error that rounding out to bf16 leaves, in fp16 (2^-11 each) they add 2% to it.
 // fp16's range is met by powers of two, which round nothing: a scale for each query row (taken
 // out of q), and for each 128 tokens of a head one for its keys and one for its values, set by
-// the largest magnitude.  The softmax then works on x + fv, fv the exponent of the tile's value
-// scale, so that the weights it hands to the product carry that scale; sums divide it out again.
+// the largest magnitude; where the tokens' largest magnitudes lie further apart than 2^8, one for
+// each token instead, so that none is rounded away beside another one, which a query need not even
+// see.  The softmax then works on x + fv, fv the exponent of the value scale, so that the weights
+// it hands to the product carry that scale; sums divide it out again.
 //
 // up_project_kernel: keys and values of every (128 tokens, head), [128, 512] x W_h^T [512, 256],
 //   written as the 128-byte-swizzled images that the attention's MMAs read, so that it fetches
@@ -50,6 +52,13 @@ constexpr int kKvBytes = 5 * kChunk;          // keys (three chunks), then value
 constexpr uint64_t kDrainNs = 200ull * 1000 * 1000;
 constexpr float kUnset = -1e38f;              // reference of a row without a token so far
 constexpr float kLift = 7.f;                  // weights reach 2^(8 + 7): the upper end of fp16's range
+// Largest distance, in powers of two, between the tokens of a tile that share a scale: a token that
+// far below the largest is held to 2^-31 of its own largest value, and every weight to 2^-22 of the
+// largest weight times value.  A tile beyond it costs its softmax two more passes over the
+// scores: 8,192 tokens x 96 heads take 2.16 ms without one, 2.31 with one that all queries see
+// and 6.7 with nothing else, where one scale a tile took 2.14 and rounded the smaller tokens away.
+constexpr int kSpread = 8;
+constexpr float kOwnScale = 1000.f;           // in Ws::scale: the tokens' scales are in Ws::own
 constexpr int64_t kL2Bytes = 48ll << 20;      // keys and values that a group of heads may take
 
 struct Pair {           // up to 256 queries of a sequence
@@ -85,7 +94,8 @@ struct Ws {
   Steps* step;          // [max tiles]
   Merge* merge;         // [blocks]
   int2* spoiled;        // [T * H] a row of out to compute again, and the entry before it of the same warp
-  float2* scale;        // [max tiles][H] exponents of the key and value scales
+  float2* scale;        // [max tiles][H] exponents of the key and value scales, or kOwnScale
+  float2* own;          // [max tiles][H][128] of the tokens, where they have scales of their own
   float2* ml;           // [2 * blocks][256] reference and sum of a piece's rows
   float* o;             // [2 * blocks][256][128]
   uint8_t* kv;          // [max tiles][H][kKvBytes]
@@ -114,6 +124,7 @@ Ws carve(void* base, int64_t T, int64_t B, int64_t H, int64_t cache_rows, int bl
   w.merge = reinterpret_cast<Merge*>(take(sizeof(Merge) * blocks));
   w.spoiled = reinterpret_cast<int2*>(take(sizeof(int2) * T * H));
   w.scale = reinterpret_cast<float2*>(take(sizeof(float2) * w.max_tiles * H));
+  w.own = reinterpret_cast<float2*>(take(sizeof(float2) * w.max_tiles * H * kTok));
   w.ml = reinterpret_cast<float2*>(take(sizeof(float2) * kPair * 2 * blocks));
   w.o = reinterpret_cast<float*>(take(int64_t(4) * kPair * 128 * 2 * blocks));
   w.kv = take(w.max_tiles * H * kKvBytes);
@@ -312,7 +323,7 @@ struct UpMisc {
   uint64_t full[kUpStages], empty[kUpStages], a_full, a_empty, acc_full[2], acc_empty[2], mma_done;
   uint32_t tmem;
   int abort;
-  float red[8];
+  float2 red[8];          // largest and smallest of the tokens' largest magnitudes, of a warp
 };
 constexpr int kUpSmem = kUpA + kUpStages * kUpStage + sizeof(UpMisc);
 static_assert(kUpSmem <= 232448, "shared memory per block");
@@ -461,12 +472,21 @@ __global__ void __launch_bounds__(kUpThreads, 1)
         }
       }
       if (r >= valid) top = 0.f;
-      top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-      if (lane == 0) mi.red[warp - 4] = top;
+      // tokens without a value but zeros (and what is not finite) fit any scale
+      const uint32_t hi = __reduce_max_sync(0xffffffffu, __float_as_uint(top));
+      const uint32_t lo = __reduce_min_sync(0xffffffffu, top > 0.f ? __float_as_uint(top) : 0x7F800000u);
+      if (lane == 0) mi.red[warp - 4] = make_float2(__uint_as_float(hi), __uint_as_float(lo));
       named_bar_sync(1 + part, 128);
-      top = fmaxf(fmaxf(mi.red[4 * part], mi.red[4 * part + 1]), fmaxf(mi.red[4 * part + 2], mi.red[4 * part + 3]));
+      float most = 0.f, least = INFINITY;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const float2 v = mi.red[4 * part + k];
+        most = fmaxf(most, v.x);
+        least = fminf(least, v.y);
+      }
       named_bar_sync(1 + part, 128);
-      const int f = scale_exponent(top, part == 0 ? kLowestFactor : kLowestValue);
+      const bool own = static_cast<int>(__float_as_uint(most) >> 23) - static_cast<int>(__float_as_uint(least) >> 23) > kSpread;
+      const int f = scale_exponent(own ? top : most, part == 0 ? kLowestFactor : kLowestValue);
       const float inv = pow2(-f);
       uint8_t* const dst = w.kv + (tile * H + h) * kKvBytes + part * 3 * kChunk + r * 128;
 #pragma unroll 1
@@ -497,7 +517,11 @@ __global__ void __launch_bounds__(kUpThreads, 1)
           store_units(dst + 2 * kChunk, r, u, t[0], t[1]);
         }
       }
-      if (r == 0) (part == 0 ? w.scale[tile * H + h].x : w.scale[tile * H + h].y) = static_cast<float>(f);
+      if (r == 0) (part == 0 ? w.scale[tile * H + h].x : w.scale[tile * H + h].y) = own ? kOwnScale : static_cast<float>(f);
+      if (own) {
+        float2* const t = w.own + (tile * H + h) * kTok + r;
+        (part == 0 ? t->x : t->y) = static_cast<float>(f);
+      }
     }
   }
   tc_fence_before();
@@ -547,6 +571,16 @@ __device__ __forceinline__ void item_of(const Params& p, uint32_t pairs, uint32_
   *head = g * group + rest % in;
 }
 
+// Exponents of token r's key and value scale in block blk = (tile, head) whose entry of Ws::scale is sc
+__device__ __forceinline__ float2 token_scale(const Ws& w, float2 sc, int64_t blk, int r) {
+  if (sc.x == kOwnScale || sc.y == kOwnScale) {
+    const float2 t = w.own[blk * kTok + r];
+    if (sc.x == kOwnScale) sc.x = t.x;
+    if (sc.y == kOwnScale) sc.y = t.y;
+  }
+  return sc;
+}
+
 // Row (token, head) of out over its own prefix, by a warp: scores of 32 tokens at a time, a lane
 // each, then four of the 128 dims a lane.  For rows that a NaN or an infinity beside their prefix
 // spoiled (0 * NaN).  It may take long, so it runs where nobody waits for the warp.
@@ -558,8 +592,9 @@ __device__ __noinline__ void redo_row(const Params& p, int row) {
   for (int s0 = 0; s0 <= lim; s0 += 32) {
     const int64_t blk = static_cast<int64_t>(tile0 + s0 / kTok) * p.H + head;
     const uint8_t* const kv = p.ws.kv + blk * kKvBytes;
-    const float2 sc = p.ws.scale[blk];
-    const int r0 = s0 % kTok, r = r0 + lane, n = lim - s0 < 31 ? lim - s0 + 1 : 32;
+    const int r0 = s0 % kTok, r = r0 + lane;
+    const float2 sc = token_scale(p.ws, p.ws.scale[blk], blk, r);
+    const int n = lim - s0 < 31 ? lim - s0 + 1 : 32;
     float x = -INFINITY;
     if (lane < n) {
       x = 0.f;
@@ -602,6 +637,42 @@ __device__ __noinline__ void redo_row(const Params& p, int row) {
   }
   const float inv = l != 0.f ? 1.f / l : 0.f;
   reinterpret_cast<uint2*>(p.out + static_cast<int64_t>(row) * 128)[lane] = make_uint2(pack2(o[0] * inv, o[1] * inv), pack2(o[2] * inv, o[3] * inv));
+}
+
+// A tile whose tokens have scales of their own: the row's scores in TMEM become x + fv of each token
+// (log2 units, -inf behind `rel`), and returned are the largest x and the sum of 2^(x - largest).
+__device__ __noinline__ float2 own_scores(const Params& p, float2 sc, int64_t blk, uint32_t ts, int fq, int rel) {
+  const int lane = threadIdx.x & 31;
+  float2 s[4];                                  // of tokens lane, lane + 32, ...
+#pragma unroll
+  for (int j = 0; j < 4; ++j) s[j] = token_scale(p.ws, sc, blk, lane + 32 * j);
+  float top = -INFINITY, sum = 0.f;
+#pragma unroll 1
+  for (int c = 0; c < kTok; c += 16) {
+    const float mine = c < 32 ? s[0].x : c < 64 ? s[1].x : c < 96 ? s[2].x : s[3].x;
+    float x[16];
+    tmem_ld16(ts + c, x);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      const int f = static_cast<int>(__shfl_sync(0xffffffffu, mine, (c & 16) + k));
+      x[k] = c + k <= rel ? x[k] * score_factor(p.scale, fq + f) : -INFINITY;
+      top = fmaxf(top, x[k]);
+    }
+    tmem_st16(ts + c, x);
+  }
+#pragma unroll 1
+  for (int c = 0; c < kTok; c += 16) {
+    const float mine = c < 32 ? s[0].y : c < 64 ? s[1].y : c < 96 ? s[2].y : s[3].y;
+    float x[16];
+    tmem_ld16(ts + c, x);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) {
+      sum += x[k] == -INFINITY ? 0.f : ex2_approx(x[k] - top);
+      x[k] += __shfl_sync(0xffffffffu, mine, (c & 16) + k);
+    }
+    tmem_st16(ts + c, x);
+  }
+  return make_float2(top == -INFINITY ? 0.f : top, sum);
 }
 
 __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_constant__ Params p) {
@@ -875,11 +946,16 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
       if (n > 0) sc = scales[0];
 #pragma unroll 1
       for (int t = 0; t < n; ++t, ++done) {
-        const float ak = score_factor(p.scale, fq + static_cast<int>(sc.x)), fv = sc.y;
+        const bool own = sc.x == kOwnScale || sc.y == kOwnScale;
+        float ak = 1.f, fv = 0.f;
+        if (!own) ak = score_factor(p.scale, fq + static_cast<int>(sc.x)), fv = sc.y;
+        const float2 here = sc;
         if (t + 1 < n) sc = scales[static_cast<int64_t>(t + 1) * p.H];
         const int pos0 = (pc.t0 + t) * kTok;
         ok = ok && __all_sync(0xffffffffu, mbar_wait(&mi.s_full[i], done & 1, wc));
         tc_fence_after();
+        float2 sums = make_float2(0.f, 0.f);
+        if (own) sums = own_scores(p, here, static_cast<int64_t>(pc.pr.tile0 + pc.t0 + t) * p.H + pc.head, ts, fq, lim - pos0);
         uint32_t x[4][32];
 #pragma unroll
         for (int c = 0; c < 4; ++c) tmem_ld_32cols(ts + 32 * c, x[c]);
@@ -901,9 +977,11 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
         if (__any_sync(0xffffffffu, top > m + 8.f)) {
           // some row's reference rises
           const float now = top > m + 8.f ? top : m;
-          const float f = ex2_approx(m - now);
+          // the sum of the weights in two halves: it carries no value scale, so it lasts where the
+          // exponents of two tiles' values lie further apart than fp32 reaches
+          const float f = ex2_approx(m - now), half = ex2_approx(0.5f * (m - now));
           m = now;
-          l *= f;
+          l = l * half * half;
           if (t > 0) {
             // the sums so far (the scores' barrier covers the products before them)
 #pragma unroll 1
@@ -958,7 +1036,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
           if (lane == 0) mbar_arrive(&mi.p_full[i][hf]);
         }
         sum[0] = __fadd2_rn(sum[0], sum[1]);
-        l = fmaf(sum[0].x + sum[0].y, pow2(-static_cast<int>(fv)), l);
+        l = own ? fmaf(sums.y, ex2_approx(sums.x + kLift - m), l) : fmaf(sum[0].x + sum[0].y, pow2(-static_cast<int>(fv)), l);
       }
       theirs += other;
       if (n > 0) {
@@ -1073,8 +1151,10 @@ __global__ void __launch_bounds__(kMergeThreads) merge_expanded_kernel(const __g
       for (int r = 0; r < kMergeRows; ++r) {
         if (v[r].y == 0.f) continue;          // no token of the row in this piece: nothing was stored
         const float now = fmaxf(m[r], v[r].x), f0 = ex2_approx(m[r] - now), f1 = ex2_approx(v[r].x - now);
+        const float m_was = m[r];
         m[r] = now;
-        l[r] = fmaf(l[r], f0, v[r].y * f1);
+        const float h0 = ex2_approx(0.5f * (m_was - now)), h1 = ex2_approx(0.5f * (v[r].x - now));
+        l[r] = fmaf(l[r] * h0, h0, v[r].y * h1 * h1);
         o[r].x = fmaf(o[r].x, f0, c[r].x * f1);
         o[r].y = fmaf(o[r].y, f0, c[r].y * f1);
         o[r].z = fmaf(o[r].z, f0, c[r].z * f1);

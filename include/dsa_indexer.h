@@ -352,8 +352,8 @@ dsa_status_t dsa_indexer_latent_attention_fp4(dsa_indexer_t h, int64_t T, const 
                                               void* workspace, int64_t workspace_bytes, void* stream);
 
 /* Bytes of workspace of dsa_indexer_latent_attention_expanded (-1 for a bad argument): the keys
- * and values of all heads, 640 bytes a cache row and head with every sequence's rows filled up to
- * 128 ((cache_rows / 128 + min(B, T) + 1) * n_heads * 81,920 bytes), 8 bytes a query and head, and some
+ * and values of all heads, 648 bytes a cache row and head with every sequence's rows filled up to
+ * 128 ((cache_rows / 128 + min(B, T) + 1) * n_heads * 82,952 bytes), 8 bytes a query and head, and some
  * 40 MB more. */
 int64_t dsa_indexer_latent_expanded_workspace(dsa_indexer_t h, int64_t T, int32_t B, int32_t n_heads,
                                               int64_t cache_rows);
@@ -365,8 +365,12 @@ int64_t dsa_indexer_latent_expanded_workspace(dsa_indexer_t h, int64_t T, int32_
  *   k[s,h] = W_ukv[h][0..127] kv[s][0..511] | kv[s][512..575],
  *   v[s,h] = W_ukv[h][128..255] kv[s][0..511],
  *   out[t,h] = sum_s softmax_s(scale * (q[t,h] . k[s,h])) v[s,h],  bf16 [T, n_heads, 128]
- * Keys and values are fp32 sums kept in fp16, each 128 tokens of a head under scales of their own
- * (powers of two); values of a row's tokens may differ by up to 2^100 in magnitude between those.
+ * Keys and values are fp32 sums kept in fp16 under powers of two, one for 128 tokens of a head, or
+ * one for each token where their largest magnitudes lie more than 2^8 apart (slower).  So a finite
+ * row, however large, costs no other row its digits, whether a query attends to it or not: a key or
+ * value is off by 2^-11 of itself or 2^-31 of its token's largest, and a weight by 2^-11 of itself or by
+ * what makes 2^-22 of the largest weight times value in out.  Values (W_ukv times latent) below 2^-88
+ * lose bits, those below 2^-98 count as 0.
  * Only rows that some query attends to are expanded, but the workspace is sized for cache_rows:
  * pass the part of the cache that holds the call's sequences, with cache_offsets counted from
  * its first row (at most 8,388,480 rows; more: DSA_ERR_UNSUPPORTED). */

@@ -232,3 +232,65 @@ def test_expanded_many_rows_beside_a_nan(dsa, ix, H):
     assert not np.any(np.isfinite(o[:10]).all(axis=2)) and not np.any(np.isfinite(o[256:306]).all(axis=2))
     b.kv = torch.nan_to_num(b.kv, 0, 0, 0)
     _check_seen(o, b, w, tokens={10, 11, 100, 127, 128, 255, 306, 307, 395})
+
+
+# ------------------------------------------------------------------------------ magnitudes side by side
+
+@pytest.mark.parametrize("v", [2.0 ** 20, 2.0 ** 30, 2.0 ** 60, 1e30, -1e30, torch.finfo(torch.bfloat16).min])
+@pytest.mark.parametrize("H", [3, 300])
+def test_expanded_a_large_row_that_only_later_queries_see(dsa, ix, v, H):
+    b, w = Batch(110, [400, 150], [400, 150], H, dim=192), _weights(110, H)
+    b.kv[200, 9] = v
+    b.kv[210] = v
+    o = _expanded(ix, b, w)
+    assert ix.device_error() == dsa.DSA_OK
+    _check_seen(o, b, w, tokens=set(range(0, 200, 7 if H == 3 else 67)) | {127, 128, 199} | set(range(400, 550, 49)))
+
+
+@pytest.mark.parametrize("exp", [9, 16, 28, 40, 60, 100])
+@pytest.mark.parametrize("n,nq,H", [(400, 130, 2), (2500, 100, 2), (400, 30, 300)])
+def test_expanded_a_large_value_of_next_to_no_weight(dsa, ix, exp, n, nq, H):
+    # channel 17 feeds the values alone, so row 150 has an ordinary key but a value 2^exp times the others'
+    b, w = Batch(111, [n], [nq], H, dim=192), _weights(111, H)
+    w[:, :128, 17] = 0
+    b.kv[150, 17] = 2.0 ** exp
+    b.q[:, :, 128:] = b.q[:, :, 128:].abs()
+    b.kv[150, 512:] = -60.0                      # score near -200: weight below 2^-250
+    o = _expanded(ix, b, w)
+    assert ix.device_error() == dsa.DSA_OK
+    _check_seen(o, b, w, tokens=set(range(0, nq, 13)))
+
+
+@pytest.mark.parametrize("exp", [9, 16, 28, 40, 60])
+def test_expanded_a_large_key_of_no_weight(dsa, ix, exp):
+    b, w = Batch(112, [390], [140], 2, dim=192), _weights(112, 2)
+    b.q[:, :, 128:] = b.q[:, :, 128:].abs()
+    b.kv[260, 512:] = -2.0 ** exp
+    o = _expanded(ix, b, w)
+    assert ix.device_error() == dsa.DSA_OK
+    _check_seen(o, b, w)
+
+
+@pytest.mark.parametrize("step", [0.2, 1.0])
+def test_expanded_every_value_larger_than_those_before(dsa, ix, step):
+    # values grow by 2^step from row to row (2^-75 to 2^75 with the larger step), scores are
+    # ordinary: a query's output is made of the rows just before it, all far below the tile's largest
+    b, w = Batch(113, [150], [150], 2, dim=192), _weights(113, 2)
+    w[:, :128] = 0
+    b.kv[:, :512] = (b.kv[:, :512].float() * torch.exp2(step * (torch.arange(150.0) - 75))[:, None]).to(torch.bfloat16)
+    if step == 1.0:
+        b.kv[:10] = 0                            # and below 2^-60 a value may lose bits
+    o = _expanded(ix, b, w)
+    assert ix.device_error() == dsa.DSA_OK
+    _check_seen(o, b, w, tokens=set(range(20 if step == 1.0 else 0, 150)))
+
+
+def test_expanded_zero_values_beside_large_ones(dsa, ix):
+    # the sum of the weights spans what lies between a tile of zero values and one of 2^110
+    b, w = Batch(114, [384], [128], 2, dim=192), _weights(114, 2)
+    w[:, :128] = 0                               # scores from the rope part alone
+    b.kv[:256, :512] = 0
+    b.kv[256:, :512] = (b.kv[256:, :512].float() * 2.0 ** 110).to(torch.bfloat16)
+    o = _expanded(ix, b, w)
+    assert ix.device_error() == dsa.DSA_OK
+    _check_seen(o, b, w)
