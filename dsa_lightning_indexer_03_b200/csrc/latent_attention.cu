@@ -23,9 +23,10 @@
 //             into fp16 too (their rope part, and the rope keys, stay bf16: an MMA of their own).
 //   softmax   12 warps, a thread per token and a third of the rows.  The reference m of a row is
 //             its running maximum, raised only when a score exceeds it by more than 8 (log2 units,
-//             so weights stay below 256): most tiles then need no maximum over the tokens, which
-//             lie across threads, only a vote.  Sums are taken over the warp in every tile, over
-//             the warps at the end.  Weights go to shared memory in the values' type.
+//             so weights stay below 256, or 2^15 in fp16, whose weights start at 2^7 to keep light
+//             ones): most tiles then need no maximum over the tokens, which lie across threads, only
+//             a vote.  Sums are taken over the warp in every tile, over the warps at the end.
+//             Weights go to shared memory in the values' type.
 //   MMA       two warps, one for the scores and one for the values, so that the scores of the
 //             next tile run beside the values of this one, and the softmax under both.
 // Work: plan_kernel lists the groups and their tiles; the blocks take equal shares of all tiles
@@ -71,6 +72,9 @@ struct Roles {
   // chunks of scores at a time, so that two such pairs make the ring, and values come by 32 tokens.
   static constexpr int kS = FP4 ? 4 : 3, kV = 2, kVTok = FP4 ? 32 : 64, kVStage = kVTok * 256;
   static_assert(kS * kStage + kV * kVStage <= kRings, "rings");
+  // A row's reference lies this far (log2 units) below its maximum: fp16 weights use the range
+  // up to 2^15, so that 131,072 tokens of 2^-26 of the heaviest still count; bf16 has fp32's range.
+  static constexpr float kLift = FP4 ? 7.f : 0.f;
 };
 constexpr uint32_t kTmemS = 4 * kRows;       // O^T block j at 96 j, the scores behind them
 constexpr uint64_t kDrainNs = 200ull * 1000 * 1000;
@@ -840,7 +844,7 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
 #pragma unroll
           for (int c = 0; c < kCols / 2; ++c) top = fmaxf(top, fmaxf(y[c].x, y[c].y));
         }
-        if (named_bar_or(bar_id, 128, top > 8.f)) {
+        if (named_bar_or(bar_id, 128, top > R::kLift + 8.f)) {
           // some row's reference rises: the tile's maximum of every row, over the tokens
           scores();
           {
@@ -855,7 +859,7 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
             for (int k = 0; k < 4; ++k) v = fmaxf(v, mi.red[4 * wg + k][wtid]);
             v *= FP4 ? mi.qs[segs & 1][c0 + wtid] : p.scale_log2;
             const float old = -mi.nm[c0 + wtid];
-            const float now = v > old + 8.f ? v : old;
+            const float now = v > old + R::kLift + 8.f ? v - R::kLift : old;
             mi.nm[c0 + wtid] = -now;
             mi.f[c0 + wtid] = ex2_approx(old - now);
           }
@@ -886,7 +890,7 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
         if (lane == 0) mbar_arrive(&mi.s_empty);
         // weights: 2^y, summed before their rounding to the values' type, the operand type of the
         // product (lse keeps fp32's precision; out gets one rounding a weight, of up to 2^-8 in
-        // bf16; in fp16 2^-11, and 2^-25 where a weight is below 2^-14 of the largest)
+        // bf16; in fp16 2^-11, and 2^-32 of the largest where a weight is below 2^-21 of it)
         uint32_t pk[kCols / 2];
         if (nc > 0) {
 #pragma unroll

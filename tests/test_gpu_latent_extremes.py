@@ -294,3 +294,28 @@ def test_expanded_zero_values_beside_large_ones(dsa, ix):
     o = _expanded(ix, b, w)
     assert ix.device_error() == dsa.DSA_OK
     _check_seen(o, b, w)
+
+
+# ------------------------------------------------------------------------------ light weights
+
+@pytest.mark.parametrize("n", [4000, 60000])
+@pytest.mark.parametrize("split", [False, True])
+def test_4bit_many_light_tokens_beside_one_heavy(dsa, ix, n, split):
+    # token 0 has score 18, the others 0: weights of 2^-26 of the heavy one, which together carry the
+    # whole output (the heavy token's latent is zero)
+    b = Batch(120, [n], [1], 16)
+    b.q.zero_()
+    b.q[:, :, 512] = 1.0
+    b.kv[:, :512] = b.kv[:1, :512]
+    b.kv[:, 512:] = 0
+    b.kv[0, :512], b.kv[0, 512] = 0, 18.0
+    kv4 = ix.quantize_latent_fp4(b.kv.to(DEV))
+    val = f64(ix.dequantize_latent_fp4(kv4))
+    qo, co = b.qo.to(DEV), b.co.to(DEV)
+    idx = torch.arange(n, dtype=torch.int32, device=DEV)[None] if split else None
+    o, lse = ix.latent_attention_fp4(b.q.to(DEV), kv4, b.pos.to(DEV), qo, co, 1.0, idx=idx)
+    assert ix.device_error() == dsa.DSA_OK
+    ref, lref, mag = oracle.latent_attention(f64(b.q), val, b.pos.numpy(), b.qo.numpy(), b.co.numpy(), 1.0)
+    tol = 1.01 * U * np.abs(ref) + (1.05 * F + 2.0 ** -16) * (mag + np.abs(ref)) + n * 2.0 ** -32 * np.abs(val[1:, :512]).max(0)
+    assert np.all(np.abs(f64(o) - ref) <= tol)
+    assert np.all(np.abs(f64(lse) - lref) <= 1e-5)
