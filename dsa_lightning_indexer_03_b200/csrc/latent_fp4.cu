@@ -70,12 +70,16 @@ __global__ void __launch_bounds__(kFp4Warps * 32) quantize_latent_fp4_kernel(int
     const uint32_t rope = reinterpret_cast<const uint32_t*>(src)[kLatV / 2 + lane];
     const uint32_t u[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
     float v[16], amax = 0.f;
+    uint32_t top = 0u;                    // magnitudes of bf16 pairs compare as integers, NaN the largest
 #pragma unroll
     for (int k = 0; k < 8; ++k) {
+      top = __vmaxu2(top, u[k] & 0x7FFF7FFFu);
       v[2 * k] = bf_lo(u[k]);
       v[2 * k + 1] = bf_hi(u[k]);
       amax = fmaxf(amax, fmaxf(fabsf(v[2 * k]), fabsf(v[2 * k + 1])));
     }
+    // codes cannot hold what is not finite: the row is written all the same, and reported
+    if ((top & 0x7F80u) == 0x7F80u || (top >> 23) == 0xFFu) atomicOr(err, kErrBounds);
     const uint32_t sc = e4m3_code(fminf(__fdiv_rn(amax, 6.f), 448.f));
     const float s = e4m3_value(sc);
     const float inv = s > 0.f ? __fdiv_rn(1.f, s) : 0.f;

@@ -353,7 +353,8 @@ class Indexer:
 
     def quantize_latent_fp4(self, kv, out=None, rows=None, stream=None):
         """4-bit rows (uint8 [n, 416]) of bf16 latent rows kv [n, 576]; with out (a cache) and
-        rows (int64 [n], distinct), row i goes to out[rows[i]].  Returns out."""
+        rows (int64 [n], distinct), row i goes to out[rows[i]].  Returns out.  A latent that is not
+        finite shows in device_error()."""
         dev = self.device
         _need(kv, "kv", torch.bfloat16, dev)
         if kv.dim() != 2 or kv.shape[1] != 576:

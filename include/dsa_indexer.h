@@ -328,7 +328,9 @@ dsa_status_t dsa_indexer_latent_attention(dsa_indexer_t h, int64_t T, const void
  * block of 16 values, and the 64-value rope key in bf16 (128 bytes).  A block's scale is
  * s = e4m3(min(amax / 6, 448)) and its codes e2m1(x / s), to nearest, ties to the even code,
  * saturating at 6 s; s = 0 stores zeros.  The value stood for is code * s, exact in bf16.
- * kv bf16 [n, 576] holds finite values. */
+ * kv bf16 [n, 576]; a latent value that is not finite has no code: its row is written, the 16
+ * values of its block then mean nothing, and the call sets DSA_ERR_DEVICE_BOUNDS (a rope value
+ * is stored as it is, whatever it holds). */
 
 /* Row i of kv goes to row rows[i] of out (rows int64 [n], distinct), or to row i when rows is
  * NULL.  A row outside [0, out_rows) is not written and sets DSA_ERR_DEVICE_BOUNDS. */

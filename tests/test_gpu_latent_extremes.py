@@ -319,3 +319,30 @@ def test_4bit_many_light_tokens_beside_one_heavy(dsa, ix, n, split):
     tol = 1.01 * U * np.abs(ref) + (1.05 * F + 2.0 ** -16) * (mag + np.abs(ref)) + n * 2.0 ** -32 * np.abs(val[1:, :512]).max(0)
     assert np.all(np.abs(f64(o) - ref) <= tol)
     assert np.all(np.abs(f64(lse) - lref) <= 1e-5)
+
+
+# ------------------------------------------------------------------------------ rows that are not finite
+
+@pytest.mark.parametrize("v", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("at", [(0, 0), (5, 17), (8, 511), (3, 300)])
+def test_4bit_rows_report_what_is_not_finite(dsa, ix, v, at):
+    g = torch.Generator().manual_seed(8)
+    x = torch.randn((9, 576), generator=g).to(torch.bfloat16)
+    want = ix.quantize_latent_fp4(x.to(DEV))
+    assert ix.device_error() == dsa.DSA_OK
+    x[at] = v
+    got = ix.quantize_latent_fp4(x.to(DEV))
+    assert ix.device_error() == dsa.DSA_ERR_DEVICE_BOUNDS
+    keep = [i for i in range(9) if i != at[0]]
+    assert torch.equal(got[keep], want[keep])
+    # the other blocks of the row are as they were
+    blk = at[1] // 16
+    codes = torch.ones(256, dtype=torch.bool)
+    codes[8 * blk:8 * blk + 8] = False
+    assert torch.equal(got[at[0], :256].cpu()[codes], want[at[0], :256].cpu()[codes])
+    # a rope key is stored as it is, whatever it holds
+    x = torch.randn((2, 576), generator=g).to(torch.bfloat16)
+    x[1, 570] = v
+    back = ix.dequantize_latent_fp4(ix.quantize_latent_fp4(x.to(DEV)))
+    assert ix.device_error() == dsa.DSA_OK
+    assert torch.equal(back[:, 512:].cpu().view(torch.int16), x[:, 512:].contiguous().view(torch.int16))
