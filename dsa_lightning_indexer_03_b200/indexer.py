@@ -308,6 +308,8 @@ class Indexer:
             if torch.cuda.current_device() == self.device.index:
                 return contextlib.nullcontext()
             return torch.cuda.device(self.device)
+        if stream.device != self.device:   # its kernels would run on a GPU that does not hold the tensors
+            raise ValueError(f"stream must be on {self.device}, got {stream.device}")
         return torch.cuda.stream(stream)
 
     def _latent(self, q, kv, fp4, positions, q_seq_offsets, cache_offsets, scale, idx, out, lse, stream):
