@@ -9,7 +9,8 @@ Readings ('Latent attention (MLA)' row: 512-dim latent plus a 64-dim shared key 
     (o = 0, lse = -inf); score = scale * (q . row) over the 576 cached values, value = latent;
   * expanded: a head's key is the bf16 up-projection of the latent (128 values) followed by the
     row's 64 rope values, its value the bf16 up-projection (128 values); the library keeps both
-    in fp16 instead, and bounds that use this form allow a step of bf16 a value;
+    in fp16 instead, and bounds that use this form allow a step of bf16 a value (rounded=False
+    leaves both in float64);
   * 4-bit rows: blocks of 16 latent values share the scale e4m3(min(amax / 6, 448)); codes are
     e2m1, nearest, ties to even, saturating; the rope key stays bf16.
 """
@@ -63,18 +64,20 @@ def latent_attention(q, kv, positions, q_seq_offsets, cache_offsets, scale, idx=
     return o, lse, mag
 
 
-def expand(kv, W_ukv):
-    """Keys [rows, H, 192] and values [rows, H, 128] of latent rows, rounded to bf16."""
+def expand(kv, W_ukv, rounded=True):
+    """Keys [rows, H, 192] and values [rows, H, 128] of latent rows, rounded to bf16 or not."""
     H = W_ukv.shape[0]
-    up = bf16_round(np.einsum("sc,hdc->shd", kv[:, :512], W_ukv))
+    up = np.einsum("sc,hdc->shd", kv[:, :512], W_ukv)
+    if rounded:
+        up = bf16_round(up)
     rope = np.broadcast_to(kv[:, None, 512:], (kv.shape[0], H, 64))
     return np.concatenate((up[:, :, :128], rope), axis=2), up[:, :, 128:]
 
 
-def latent_attention_expanded(q, kv, W_ukv, positions, q_seq_offsets, cache_offsets, scale):
+def latent_attention_expanded(q, kv, W_ukv, positions, q_seq_offsets, cache_offsets, scale, rounded=True):
     """q [T, H, 192]; returns o [T, H, 128] and sum_j w_j |v_j|."""
     T, H, _ = q.shape
-    k, v = expand(kv, W_ukv)
+    k, v = expand(kv, W_ukv, rounded)
     o = np.full((T, H, 128), np.nan)
     mag = np.full((T, H, 128), np.nan)
     for t in range(int(q_seq_offsets[0]), int(q_seq_offsets[-1])):
