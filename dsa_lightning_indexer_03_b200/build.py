@@ -21,6 +21,8 @@ SOURCES = ["api.cu", "proj.cu", "score_topk.cu", "noalloc.cu", "reuse.cu", "spar
 HEADERS = ["common.cuh", "handle.h", "kernels.h", "latent.h", "latent_mma.cuh"]
 # what the recorded traffic figures depend on: all but the latent-cache operators
 PROFILED = [f for f in SOURCES + HEADERS if not f.startswith("latent")]
+# and the counters recorded for the latent-cache operators
+LATENT = ["common.cuh"] + [f for f in SOURCES + HEADERS if f.startswith("latent")]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", os.path.join(ROOT, "include")]
 
@@ -39,13 +41,13 @@ def _inputs():
     return files
 
 
-def source_hash() -> str:
-    """Short hash of the profiled kernels' code: ties recorded profile figures to the kernels they
+def source_hash(files=None) -> str:
+    """Short hash of the code in files (PROFILED by default): ties recorded profile figures to the kernels they
     measured.  Comments and blank lines are left out, so editing a comment keeps the figures."""
     import hashlib
     import re
     h = hashlib.sha256()
-    for f in sorted(PROFILED):
+    for f in sorted(PROFILED if files is None else files):
         with open(os.path.join(CSRC, f)) as fh:
             text = fh.read()
         text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)

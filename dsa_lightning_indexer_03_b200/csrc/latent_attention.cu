@@ -527,8 +527,9 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
       }
     };
     // L2 keeps a tile between its two readings: without these hints 1.8 times the cache's bytes came
-    // from memory (64 sequences of 8,192 tokens), and the decode batch of 64 took 1.81 ms, not 1.44.
-    // Fetching the next tile into L2 as well made room for less of that and took 1.58 ms.
+    // from memory (64 sequences of 8,192 tokens), and the decode batch of 64 takes 1.59 ms, not 1.49
+    // (a prompt chunk, whose cache L2 holds anyway, 743 us, not 754).  Fetching the next tile into L2
+    // as well made room for less of that and was a tenth slower.
     const uint64_t keep = l2_policy_evict_last(), drop = l2_policy_evict_first();
     uint32_t it = 0;        // stages of the warp's ring so far
     uint32_t segs = 0;      // pieces so far

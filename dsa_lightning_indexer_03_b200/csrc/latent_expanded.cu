@@ -33,7 +33,7 @@
 // Bound: the tensor core, 128 x 128 x (192 + 128) products in 1,280 cycles, and close behind
 // it the 16,384 exponentials of those weights (1,024 cycles).  Measured: a step of both tiles takes
 // 3,950 cycles, the chain of one of them (scores 1,400, maximum 550, weights 1,500, rest of the
-// sums 500), and changing items 15,000; 8,192 tokens x 96 heads 2.18 ms in a row of calls, of
+// sums 500), and changing items 15,000; 8,192 tokens x 96 heads 2.20 ms in a row of calls, of
 // which the up-projection is 0.21 (1.37 and 0.13 at the measured tensor rate).
 
 #include <cuda_fp16.h>

@@ -399,7 +399,8 @@ class Indexer:
                                   stream=None):
         """Attention in the expanded form, for prompts: q bf16 [T, H, 192], the cache rows of the
         call's sequences kv_cache bf16 [rows, 576], W_ukv bf16 [H, 256, 512] (each head's 128 key
-        rows, then its 128 value rows); returns out bf16 [T, H, 128]."""
+        rows, then its 128 value rows); returns out bf16 [T, H, 128].  Allocates 648 bytes a row of
+        kv_cache and head: pass the part of the cache that the call needs."""
         T, H, B = self._latent_common(q, 192, positions, q_seq_offsets, cache_offsets, kv_cache, torch.bfloat16, 576)
         _need(W_ukv, "W_ukv", torch.bfloat16, self.device)
         if W_ukv.shape != (H, 256, 512):
