@@ -346,7 +346,9 @@ dsa_status_t dsa_indexer_dequantize_latent_fp4(dsa_indexer_t h, int64_t n, const
 /* dsa_indexer_latent_attention over a 4-bit cache.  k_sel < 0: dense (idx is not read).
  * k_sel >= 0: over the indexer's selection, idx int32 [T, k_sel], positions in the query's
  * sequence, -1 = no token, a repeated position counting once per entry (positions may be NULL);
- * an entry at or past its sequence's row count is skipped and sets DSA_ERR_DEVICE_BOUNDS. */
+ * an entry at or past its sequence's row count is skipped and sets DSA_ERR_DEVICE_BOUNDS.  Queries
+ * are scaled to magnitudes up to 2^15 for the scores, so a rope key that a query attends to should
+ * stay below 2^100 (beyond about 2^106 the fp32 score overflows, whatever the query). */
 dsa_status_t dsa_indexer_latent_attention_fp4(dsa_indexer_t h, int64_t T, const void* q, int32_t n_heads,
                                               const void* kv_cache_fp4, int64_t cache_rows, const int32_t* positions,
                                               const int32_t* q_seq_offsets, int32_t B, const int64_t* cache_offsets,

@@ -346,3 +346,76 @@ def test_4bit_rows_report_what_is_not_finite(dsa, ix, v, at):
     back = ix.dequantize_latent_fp4(ix.quantize_latent_fp4(x.to(DEV)))
     assert ix.device_error() == dsa.DSA_OK
     assert torch.equal(back[:, 512:].cpu().view(torch.int16), x[:, 512:].contiguous().view(torch.int16))
+
+
+# ------------------------------------------------------------------------------ together
+
+@pytest.mark.parametrize("n,nq,H", [(700, 300, 3), (400, 30, 300)])      # shares of steps; whole items
+def test_expanded_slow_paths_on_two_streams_and_in_graphs(dsa, ix, n, nq, H):
+    # a tile of own scales and a row to be computed again, at once on two streams, captured twice, and
+    # replayed after the inputs lost both and got them back
+    b, w = Batch(140, [n, 90], [nq, 20], H, dim=192), _weights(140, H)
+    plain = b.kv.clone()
+    b.kv[5, 300] = 2.0 ** 40
+    b.kv[n - 3] = float("nan")
+    q, kv, pos, qo, co = b.dev("q", "kv", "pos", "qo", "co")
+    w, odd, plain = w.to(DEV), kv.clone(), plain.to(DEV)
+    call = lambda **k: ix.latent_attention_expanded(q, kv, w, pos, qo, co, SCALE, **k)  # noqa: E731
+    same = lambda x, y: torch.equal(x.view(torch.int16), y.view(torch.int16))  # noqa: E731
+    want = call()
+    kv.copy_(plain)
+    ordinary = call()
+    assert not bool(torch.isfinite(want).all()) and bool(torch.isfinite(ordinary).all())
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    kv.copy_(odd)
+    torch.cuda.synchronize()
+    outs = [call(stream=s) for s in streams * 2]
+    torch.cuda.synchronize()
+    assert all(same(want, o) for o in outs)
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            res = call()
+        graphs.append((g, res))
+    for k, (src, ref) in enumerate(((plain, ordinary), (odd, want), (odd, want), (plain, ordinary), (odd, want))):
+        kv.copy_(src)
+        g, res = graphs[k & 1]
+        g.replay()
+        torch.cuda.synchronize()
+        assert same(res, ref)
+    assert ix.device_error() == dsa.DSA_OK
+
+
+def test_batches_of_nothing(dsa, ix):
+    # queries that attend to nothing, tokens of no sequence only, sequences without rows, one idx row of -1s
+    H = 5
+    b, w = Batch(141, [50, 0], [4, 0], H), _weights(141, H).to(DEV)
+    kv4 = ix.quantize_latent_fp4(b.kv.to(DEV))
+    q, kv, co = b.dev("q", "kv", "co")
+    qe = q[:, :, :192].contiguous()
+    none = torch.full((4,), -1, dtype=torch.int32, device=DEV)
+    all_in = torch.tensor([0, 4, 4], dtype=torch.int32, device=DEV)
+    for qo in ([0, 4, 4], [0, 0, 0], [2, 2, 2], [4, 4, 4]):
+        qo = torch.tensor(qo, dtype=torch.int32, device=DEV)
+        kept = qo[0] == qo[2]
+        for call in (lambda **k: ix.latent_attention(q, kv, none, qo, co, SCALE, **k),
+                     lambda **k: ix.latent_attention_fp4(q, kv4, none, qo, co, SCALE, **k),
+                     lambda **k: ix.latent_attention_fp4(q, kv4, None, qo, co, SCALE,
+                                                         idx=torch.full((4, 130), -1, dtype=torch.int32, device=DEV), **k)):
+            out = torch.full((4, H, 512), 7.0, dtype=torch.bfloat16, device=DEV)
+            lse = torch.full((4, H), 7.0, device=DEV)
+            call(out=out, lse=lse)
+            assert bool((out == (7.0 if kept else 0.0)).all())
+            assert bool((lse == 7.0).all() if kept else torch.isneginf(lse).all())
+        out = torch.full((4, H, 128), 7.0, dtype=torch.bfloat16, device=DEV)
+        ix.latent_attention_expanded(qe, kv, w, none, qo, co, SCALE, out=out)
+        assert bool((out == (7.0 if kept else 0.0)).all())
+    # a query in a sequence without rows can only attend to nothing
+    co0 = torch.tensor([0, 0, 50], dtype=torch.int64, device=DEV)
+    out = ix.latent_attention_expanded(qe, kv, w, none, all_in, co0, SCALE)
+    assert bool((out == 0).all()) and ix.device_error() == dsa.DSA_OK
+    none[2] = 0
+    out, lse = ix.latent_attention(q, kv, none, all_in, co0, SCALE)
+    assert bool((out == 0).all()) and bool(torch.isneginf(lse).all())
+    assert ix.device_error() == dsa.DSA_ERR_DEVICE_BOUNDS
