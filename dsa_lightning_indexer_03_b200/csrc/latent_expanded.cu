@@ -640,7 +640,8 @@ __device__ __noinline__ void redo_row(const Params& p, int row) {
 }
 
 // A tile whose tokens have scales of their own: the row's scores in TMEM become x + fv of each token
-// (log2 units, -inf behind `rel`), and returned are the largest x and the sum of 2^(x - largest).
+// (log2 units, -inf behind `rel`), and returned are the largest x and the sum of 2^(x - largest)
+// (-inf and 0 for a row that sees none of the tokens: 2^-inf of any reference times 0 adds nothing).
 __device__ __noinline__ float2 own_scores(const Params& p, float2 sc, int64_t blk, uint32_t ts, int fq, int rel) {
   const int lane = threadIdx.x & 31;
   float2 s[4];                                  // of tokens lane, lane + 32, ...
@@ -672,7 +673,7 @@ __device__ __noinline__ float2 own_scores(const Params& p, float2 sc, int64_t bl
     }
     tmem_st16(ts + c, x);
   }
-  return make_float2(top == -INFINITY ? 0.f : top, sum);
+  return make_float2(top, sum);
 }
 
 __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_constant__ Params p) {

@@ -419,3 +419,19 @@ def test_batches_of_nothing(dsa, ix):
     out, lse = ix.latent_attention(q, kv, none, all_in, co0, SCALE)
     assert bool((out == 0).all()) and bool(torch.isneginf(lse).all())
     assert ix.device_error() == dsa.DSA_ERR_DEVICE_BOUNDS
+
+
+@pytest.mark.parametrize("n,nq,H", [(700, 200, 3), (400, 40, 300)])
+def test_expanded_queries_that_see_nothing_of_a_tile_of_own_scales(dsa, ix, n, nq, H):
+    # in one tile of queries some attend to nothing, some to the first rows only (with scores far below
+    # zero), some to all; the tiles of tokens that only the last see carry scales of their own
+    b, w = Batch(150, [n], [nq], H, dim=192), _weights(150, H)
+    b.q[:, :, 128:] = b.q[:, :, 128:].abs()
+    b.kv[:, 512:] = b.kv[:, 512:] * 0.125 - 60.0             # every score near -200
+    b.kv[n - 150::37, 300] = 2.0 ** 30
+    b.kv[3, 17] = 2.0 ** 12
+    b.pos[::3] = -1
+    b.pos[1::3] = torch.arange(len(b.pos[1::3])).int() % 140
+    o = _expanded(ix, b, w)
+    assert ix.device_error() == dsa.DSA_OK and np.all(o[::3] == 0)
+    _check_seen(o, b, w, tokens=set(range(0, nq, 1 if H == 3 else 7)))
