@@ -77,7 +77,7 @@ def _check_seen(o, b, w, scale=SCALE, tokens=None):
                 e = e[wt > 1e-12].max()                      # a lighter row's move does not show
                 e += 6 * np.sqrt(192) * 2.0 ** -24 * scale * np.linalg.norm(q[t, h]) * np.linalg.norm(k[wt > 1e-12], axis=1).max()
                 e += 4 * 2.0 ** -24 * np.abs(x[wt > 1e-12]).max() + 2.0 ** -20
-                tol = 1.01 * U * np.abs(ref) + (2.1 * F + 2 * np.expm1(e)) * (mag + np.abs(ref))
+                tol = 1.01 * U * np.abs(ref) + (2.1 * F + 2 * np.expm1(min(e, 300.0))) * (mag + np.abs(ref))
                 tol += m * 2.0 ** -22 * (wt * vmax).max() + 2.0 ** -30 * (wt * vmax).sum() + 1e-38
                 err = np.abs(o[t, h] - ref)
                 assert np.all(err <= tol), (t, h, err.max(), (err / tol).max())
