@@ -858,7 +858,7 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
           if (wtid < nc) {
             float v = -INFINITY;
             for (int k = 0; k < 4; ++k) v = fmaxf(v, mi.red[4 * wg + k][wtid]);
-            v *= FP4 ? mi.qs[segs & 1][c0 + wtid] : p.scale_log2;
+            v = __fmul_rn(v, FP4 ? mi.qs[segs & 1][c0 + wtid] : p.scale_log2);
             const float old = -mi.nm[c0 + wtid];
             const float now = v > old + R::kLift + 8.f ? v - R::kLift : old;
             mi.nm[c0 + wtid] = -now;
@@ -866,7 +866,17 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
           }
           named_bar_sync(bar_id, 128);
           scores();      // again: kept across the reduction they would not fit the registers
-          shift();
+          // The difference of the rounded product and the reference, which is one: next to it that is
+          // exact, however large the scores.  A lift lost in rounding makes no weight past the type's
+          // range (NaN stays).
+#pragma unroll
+          for (int c = 0; c < kCols / 2; ++c) {
+            const float k0 = FP4 ? mi.qs[segs & 1][c0 + 2 * c] : p.scale_log2, k1 = FP4 ? mi.qs[segs & 1][c0 + 2 * c + 1] : p.scale_log2;
+            y[c].x = __fadd_rn(__fmul_rn(y[c].x, k0), mi.nm[c0 + 2 * c]);
+            y[c].y = __fadd_rn(__fmul_rn(y[c].y, k1), mi.nm[c0 + 2 * c + 1]);
+            y[c].x = y[c].x > R::kLift + 8.f ? R::kLift + 8.f : y[c].x;
+            y[c].y = y[c].y > R::kLift + 8.f ? R::kLift + 8.f : y[c].y;
+          }
           l *= mi.f[c0 + lane];
           if (t > 0) {
             // the sums so far, once every earlier product has landed in them

@@ -33,7 +33,7 @@
 // Bound: the tensor core, 128 x 128 x (192 + 128) products in 1,280 cycles, and close behind
 // it the 16,384 exponentials of those weights (1,024 cycles).  Measured: a step of both tiles takes
 // 3,950 cycles, the chain of one of them (scores 1,400, maximum 550, weights 1,500, rest of the
-// sums 500), and changing items 15,000; 8,192 tokens x 96 heads 2.20 ms in a row of calls, of
+// sums 500), and changing items 15,000; 8,192 tokens x 96 heads 2.21 ms in a row of calls, of
 // which the up-projection is 0.21 (1.37 and 0.13 at the measured tensor rate).
 
 #include <cuda_fp16.h>
@@ -55,8 +55,9 @@ constexpr float kLift = 7.f;                  // weights reach 2^(8 + 7): the up
 // Largest distance, in powers of two, between the tokens of a tile that share a scale: a token that
 // far below the largest is held to 2^-31 of its own largest value, and every weight to 2^-22 of the
 // largest weight times value.  A tile beyond it costs its softmax two more passes over the
-// scores: 8,192 tokens x 96 heads take 2.16 ms without one, 2.31 with one that all queries see
-// and 6.7 with nothing else, where one scale a tile took 2.14 and rounded the smaller tokens away.
+// scores and a third that reads them back: 8,192 tokens x 96 heads take 2.18 ms without one, 2.38 with one
+// that all queries see and 7.6 with nothing else, where one scale a tile took 2.14 and rounded the
+// smaller tokens away.  Looking for such tiles costs every call 1%.
 constexpr int kSpread = 8;
 constexpr float kOwnScale = 1000.f;           // in Ws::scale: the tokens' scales are in Ws::own
 constexpr int64_t kL2Bytes = 48ll << 20;      // keys and values that a group of heads may take
@@ -640,40 +641,57 @@ __device__ __noinline__ void redo_row(const Params& p, int row) {
 }
 
 // A tile whose tokens have scales of their own: the row's scores in TMEM become x + fv of each token
-// (log2 units, -inf behind `rel`), and returned are the largest x and the sum of 2^(x - largest)
-// (-inf and 0 for a row that sees none of the tokens: 2^-inf of any reference times 0 adds nothing).
+// (log2 units, -inf behind `rel`), and returned are the largest of them and the sum of
+// 2^(x + fv - largest) / 2^fv.  The sum is taken from the rounded x + fv, as the weights are, so that what
+// fp32 loses of a large score leaves their quotient as it is.  (-inf and 0 for a row that sees none
+// of the tokens.)
 __device__ __noinline__ float2 own_scores(const Params& p, float2 sc, int64_t blk, uint32_t ts, int fq, int rel) {
   const int lane = threadIdx.x & 31;
   float2 s[4];                                  // of tokens lane, lane + 32, ...
 #pragma unroll
   for (int j = 0; j < 4; ++j) s[j] = token_scale(p.ws, sc, blk, lane + 32 * j);
+  auto pick = [&](int c) { return c < 32 ? s[0] : c < 64 ? s[1] : c < 96 ? s[2] : s[3]; };
   float top = -INFINITY, sum = 0.f;
 #pragma unroll 1
   for (int c = 0; c < kTok; c += 16) {
-    const float mine = c < 32 ? s[0].x : c < 64 ? s[1].x : c < 96 ? s[2].x : s[3].x;
+    const float2 mine = pick(c);
     float x[16];
     tmem_ld16(ts + c, x);
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
-      const int f = static_cast<int>(__shfl_sync(0xffffffffu, mine, (c & 16) + k));
-      x[k] = c + k <= rel ? x[k] * score_factor(p.scale, fq + f) : -INFINITY;
+      const int f = static_cast<int>(__shfl_sync(0xffffffffu, mine.x, (c & 16) + k));
+      const float fv = __shfl_sync(0xffffffffu, mine.y, (c & 16) + k);
+      x[k] = c + k <= rel ? fmaf(x[k], score_factor(p.scale, fq + f), fv) : -INFINITY;
       top = fmaxf(top, x[k]);
     }
     tmem_st16(ts + c, x);
   }
 #pragma unroll 1
   for (int c = 0; c < kTok; c += 16) {
-    const float mine = c < 32 ? s[0].y : c < 64 ? s[1].y : c < 96 ? s[2].y : s[3].y;
+    const float2 mine = pick(c);
     float x[16];
     tmem_ld16(ts + c, x);
 #pragma unroll
     for (int k = 0; k < 16; ++k) {
-      sum += x[k] == -INFINITY ? 0.f : ex2_approx(x[k] - top);
-      x[k] += __shfl_sync(0xffffffffu, mine, (c & 16) + k);
+      const float fv = __shfl_sync(0xffffffffu, mine.y, (c & 16) + k);
+      sum += x[k] == -INFINITY ? 0.f : ex2_approx(x[k] - top - fv);
     }
-    tmem_st16(ts + c, x);
   }
   return make_float2(top, sum);
+}
+
+// The row's scores in TMEM become x * ak + fv less its reference, -inf behind `rel`: a difference of two
+// rounded numbers, which is exact next to the reference.  (Not inlined: 128 more instructions
+// in the loop cost every call 1%.)
+__device__ __noinline__ void shift_scores(uint32_t ts, float ak, float fv, float m, int rel) {
+#pragma unroll 1
+  for (int c = 0; c < kTok; c += 16) {
+    float x[16];
+    tmem_ld16(ts + c, x);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) x[k] = c + k <= rel ? fmaf(x[k], ak, fv) - m : -INFINITY;
+    tmem_st16(ts + c, x);
+  }
 }
 
 __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_constant__ Params p) {
@@ -948,7 +966,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
 #pragma unroll 1
       for (int t = 0; t < n; ++t, ++done) {
         const bool own = sc.x == kOwnScale || sc.y == kOwnScale;
-        float ak = 1.f, fv = 0.f;
+        float ak = 1.f, fv = 0.f;              // own scales: in the scores already
         if (!own) ak = score_factor(p.scale, fq + static_cast<int>(sc.x)), fv = sc.y;
         const float2 here = sc;
         if (t + 1 < n) sc = scales[static_cast<int64_t>(t + 1) * p.H];
@@ -974,10 +992,14 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             tops[k] = fmaxf(tops[k], fmaxf(__uint_as_float(x[k][c]), __uint_as_float(x[k][c + 1])));
-        const float top = fmaf(fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])), ak, fv);
-        if (__any_sync(0xffffffffu, top > m + 8.f)) {
+        // the exponents of the weights stay below kLift + 8, in either form below: fp16 ends at 2^16
+        const float most = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+        float c2 = fv + kLift - m;
+        const bool rise = fmaxf(fmaf(most, ak, fv) - m + kLift, fmaf(most, ak, c2)) > kLift + 8.f;
+        bool exact = own;
+        if (__any_sync(0xffffffffu, rise)) {
           // some row's reference rises
-          const float now = top > m + 8.f ? top : m;
+          const float now = rise ? fmaf(most, ak, fv) : m;
           // the sum of the weights in two halves: it carries no value scale, so it lasts where the
           // exponents of two tiles' values lie further apart than fp32 reaches
           const float f = ex2_approx(m - now), half = ex2_approx(0.5f * (m - now));
@@ -994,6 +1016,18 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
               tmem_st16(to + 16 * c, o);
             }
           }
+          c2 = fv + kLift - m;
+          exact |= __any_sync(0xffffffffu, rise && fabsf(fmaf(most, ak, c2) - kLift) > 1.f);
+        }
+        if (exact) {
+          // own scales, or scores so large that the rounding of m alone moves weights out of range
+          shift_scores(ts, ak, fv, m, lim - pos0);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld_32cols(ts + 32 * c, x[c]);
+#pragma unroll
+          for (int c = 0; c < 4; ++c) tmem_ld_wait(x[c]);
+          ak = 1.f;
+          c2 = kLift;
         }
         // The exponentials of the two tiles alternate, 0 before 1 in every step; left alone the tiles
         // fall into step, both softmaxes then wait for both products and a step takes twice as long.
@@ -1008,7 +1042,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
           }
           __syncwarp();
         }
-        const float2 a2 = make_float2(ak, ak), c2 = make_float2(fv + kLift - m, fv + kLift - m);
+        const float2 a2 = make_float2(ak, ak), b2 = make_float2(c2, c2);
         float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
@@ -1016,7 +1050,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
 #pragma unroll
           for (int c = 0; c < 32; ++c) {
             const int k = 2 * hf + (c >> 4), j = 2 * (c & 15);
-            const float2 y = ffma2(make_float2(__uint_as_float(x[k][j]), __uint_as_float(x[k][j + 1])), a2, c2);
+            const float2 y = ffma2(make_float2(__uint_as_float(x[k][j]), __uint_as_float(x[k][j + 1])), a2, b2);
             const float2 e = make_float2(ex2_approx(y.x), ex2_approx(y.y));
             sum[c & 1] = __fadd2_rn(sum[c & 1], e);
             pk[c] = pack_f16(e.x, e.y);
@@ -1037,7 +1071,7 @@ __global__ void __launch_bounds__(kThreads, 1) expanded_kernel(const __grid_cons
           if (lane == 0) mbar_arrive(&mi.p_full[i][hf]);
         }
         sum[0] = __fadd2_rn(sum[0], sum[1]);
-        l = own ? fmaf(sums.y, ex2_approx(sums.x + kLift - m), l) : fmaf(sum[0].x + sum[0].y, pow2(-static_cast<int>(fv)), l);
+        l = own ? fmaf(sums.y, ex2_approx(sums.x - m + kLift), l) : fmaf(sum[0].x + sum[0].y, pow2(-static_cast<int>(fv)), l);
       }
       theirs += other;
       if (n > 0) {

@@ -435,3 +435,72 @@ def test_expanded_queries_that_see_nothing_of_a_tile_of_own_scales(dsa, ix, n, n
     o = _expanded(ix, b, w)
     assert ix.device_error() == dsa.DSA_OK and np.all(o[::3] == 0)
     _check_seen(o, b, w, tokens=set(range(0, nq, 1 if H == 3 else 7)))
+
+
+# ------------------------------------------------------------------------------ scores beyond fp32's fractions
+
+def _winners(x, margin):
+    """Rows whose largest score leads by so much that nothing but its token counts, and that token.
+    x holds -inf where a row does not look.  The others weigh e^-40 each at most, in all less than
+    1,000 * 4.3e-18 * 30 < 2e-13 of the output: LIGHT."""
+    two = torch.topk(x, 2, dim=-1)
+    lead = two.values[..., 0] - two.values[..., 1]
+    return lead > margin * x.masked_fill(torch.isinf(x), 0).abs().amax(-1) + 40, two.indices[..., 0]
+
+
+LIGHT = 2e-13
+
+
+@pytest.mark.parametrize("exp", [6, 16, 20, 23, 25, 27, 30, 40, 80])
+@pytest.mark.parametrize("spread", [False, True])
+@pytest.mark.parametrize("n,nq,H", [(700, 200, 3), (400, 40, 300)])
+def test_expanded_scores_up_to_2_to_the_80(dsa, ix, exp, spread, n, nq, H):
+    # the heaviest token has all the weight, so out is its value whatever is lost of the score: the
+    # value's rounding to fp16 (F, and 2^-31 of the value's largest), the weight's (F; its sum is not
+    # rounded) and out's (U), and the fp32 sum of the value's 512 products, a walk of 6 sqrt(512) 2^-24 |w| |c|
+    b, w = Batch(160 + exp, [n], [nq], H, dim=192), _weights(160, H)
+    b.q = (b.q.float() * 2.0 ** exp).to(torch.bfloat16)
+    if spread:
+        b.kv[::50, :512] = b.kv[::50, :512] * 2.0 ** -12             # tiles of own scales
+    o = torch.from_numpy(_expanded(ix, b, w))
+    assert ix.device_error() == dsa.DSA_OK and bool(torch.isfinite(o).all())
+    kv, q, wd = b.kv.double().to(DEV), b.q.double().to(DEV), w.double().to(DEV)
+    late = torch.arange(n, device=DEV)[None] > b.pos.to(DEV)[:, None]
+    for h in range(0, H, 1 if H == 3 else 23):
+        up = kv[:, :512] @ wd[h].t()
+        k, v = torch.cat((up[:, :128], kv[:, 512:]), 1), up[:, 128:]
+        x = (SCALE * q[:, h] @ k.t()).masked_fill(late, -torch.inf)
+        # fp16 keys move a score by up to F sum |q_d k_d|, far less than 2^-7 of the largest score
+        sure, at = _winners(x, 2.0 ** -6)
+        if exp >= 16:
+            assert int(sure.sum()) > nq // 2
+        ref = v[at][sure].cpu()
+        tol = (1.01 * U + 2.02 * F) * ref.abs() + 2.0 ** -30 * ref.abs().amax(1, keepdim=True) + LIGHT
+        walk = 6 * 512 ** 0.5 * 2.0 ** -24 * kv[at, :512].norm(dim=1)[:, None] * wd[h, 128:].norm(dim=1)[None]
+        tol += walk[sure].cpu()
+        assert bool(((o[:, h][sure.cpu()] - ref).abs() <= tol).all()), h
+
+
+@pytest.mark.parametrize("exp", [6, 16, 20, 23, 25, 27, 30, 40, 80])
+@pytest.mark.parametrize("fp4", [False, True])
+def test_absorbed_scores_up_to_2_to_the_80(dsa, ix, exp, fp4):
+    # out is the heaviest token's latent: allowed is one rounding of the weight's type and of out
+    b = Batch(170 + exp, [900, 300], [40, 3], 24)
+    b.q = (b.q.float() * 2.0 ** exp).to(torch.bfloat16)
+    q, kv, pos, qo, co = b.dev("q", "kv", "pos", "qo", "co")
+    if fp4:
+        kv4 = ix.quantize_latent_fp4(kv)
+        kv = ix.dequantize_latent_fp4(kv4)
+        o, lse = ix.latent_attention_fp4(q, kv4, pos, qo, co, SCALE)
+    else:
+        o, lse = ix.latent_attention(q, kv, pos, qo, co, SCALE)
+    assert ix.device_error() == dsa.DSA_OK and bool(torch.isfinite(o).all()) and bool(torch.isfinite(lse).all())
+    for t in range(43):
+        r0 = 0 if t < 40 else 900
+        rows = kv[r0:r0 + int(pos[t]) + 1].double()
+        x = SCALE * q[t].double() @ rows.t()
+        sure, at = _winners(x, 2.0 ** -10)
+        ref = rows[at][sure, :512]
+        wt = F if fp4 else U
+        assert bool(((o[t][sure].double() - ref).abs() <= (1.01 * U + 1.01 * wt) * ref.abs() + LIGHT).all()), t
+        assert bool(((lse[t].double() - x.amax(1)).abs() <= 2.0 ** -18 * x.abs().amax(1) + 10).all()), t
