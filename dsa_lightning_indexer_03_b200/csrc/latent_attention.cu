@@ -869,13 +869,17 @@ __global__ void __launch_bounds__(Roles<FP4>::kThreads, 1)
           // The difference of the rounded product and the reference, which is one: next to it that is
           // exact, however large the scores.  A lift lost in rounding makes no weight past the type's
           // range (NaN stays).
+          auto less = [](float x, float k, float nm) {
+            const float v = __fadd_rn(__fmul_rn(x, k), nm);
+            return v > R::kLift + 8.f ? R::kLift + 8.f : v;
+          };
 #pragma unroll
-          for (int c = 0; c < kCols / 2; ++c) {
-            const float k0 = FP4 ? mi.qs[segs & 1][c0 + 2 * c] : p.scale_log2, k1 = FP4 ? mi.qs[segs & 1][c0 + 2 * c + 1] : p.scale_log2;
-            y[c].x = __fadd_rn(__fmul_rn(y[c].x, k0), mi.nm[c0 + 2 * c]);
-            y[c].y = __fadd_rn(__fmul_rn(y[c].y, k1), mi.nm[c0 + 2 * c + 1]);
-            y[c].x = y[c].x > R::kLift + 8.f ? R::kLift + 8.f : y[c].x;
-            y[c].y = y[c].y > R::kLift + 8.f ? R::kLift + 8.f : y[c].y;
+          for (int c = 0; c < kCols / 4; ++c) {
+            const float4 m = nm4[c];
+            float4 k = make_float4(p.scale_log2, p.scale_log2, p.scale_log2, p.scale_log2);
+            if (FP4) k = qs4[c];
+            y[2 * c] = make_float2(less(y[2 * c].x, k.x, m.x), less(y[2 * c].y, k.y, m.y));
+            y[2 * c + 1] = make_float2(less(y[2 * c + 1].x, k.z, m.z), less(y[2 * c + 1].y, k.w, m.w));
           }
           l *= mi.f[c0 + lane];
           if (t > 0) {
